@@ -64,6 +64,7 @@ typedef enum waits_status {
 #define WAITS_DEV_PLAN_OVERFLOW  0x4u  /* internal: plan larger than its bound */
 #define WAITS_DEV_BAD_INDEX      0x8u  /* waits_compact saw idx outside [0, N) */
 #define WAITS_DEV_BAD_CURVE      0x10u /* a routed call's a or b was invalid for some sequence */
+#define WAITS_DEV_CACHE_FULL     0x20u /* waits_cache_reserve refused a sequence: free blocks, table or slot map too small */
 
 typedef struct waits_shape {
   int32_t nseq;             /* sequences in the packed batch, >= 1             */
@@ -386,6 +387,198 @@ waits_status waits_decode_attention(int32_t nseq, int32_t num_q_heads, int32_t n
                                     const void* K_cache, const void* V_cache,
                                     const int32_t* cache_len, float* out, float* lse,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Head norms and rotary positions of queries and keys in one pass: what
+ * stands between a layer's Q/K projections and waits_score (and a decode
+ * step's attention), which take both as the attention sees them.  Per token
+ * t and head row x of d values:
+ *   y = w * x / sqrt(mean(x^2) + eps)        (y = x where the weights are NULL)
+ *   pair i < rotary_dim / 2: angle = positions[t] * inv_freq[i],
+ *     (y1, y2) -> (y1 cos - y2 sin, y2 cos + y1 sin)
+ * with (y1, y2) = (y[i], y[i + rotary_dim / 2]), or (y[2i], y[2i + 1]) where
+ * `interleaved` is non-zero; dimensions from rotary_dim on keep y.  fp32
+ * arithmetic, one rounding to bf16 at the end.  The angle is reduced to a
+ * turn in 64-bit fixed point, so it is exact to 2^-32 of a turn at every
+ * 32-bit position.
+ *   q, k        DEVICE bf16, token t's head h at q + t * q_stride + h * d
+ *               (strides in elements, multiples of 8, at least the heads'
+ *               values: views of a fused projection's output fit); 16-byte
+ *               aligned
+ *   positions   DEVICE int32 [num_tokens], any values
+ *   inv_freq    HOST double [rotary_dim / 2], finite; read before the call returns
+ *   q_weight, k_weight  DEVICE bf16 [d], 16-byte aligned, or both NULL
+ *   q_out, k_out  as q, k with their own strides.  An output may be its own
+ *               input (same pointer and stride); any other overlap with an
+ *               input gives unspecified values.
+ * num_tokens = 0 does nothing.  head_dim 64 or 128; rotary_dim a multiple of
+ * 8 in [8, head_dim].
+ * Errors: ARG (null, misaligned, eps negative or not finite, a stride too
+ * small or not a multiple of 8, one weight without the other, an output
+ * that is its own input with another stride), SHAPE, UNSUPPORTED, CUDA.
+ */
+waits_status waits_qk_norm_rope(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                                const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const int32_t* positions, const double* inv_freq,
+                                const void* q_weight, const void* k_weight, float eps,
+                                void* q_out, int64_t q_out_stride, void* k_out,
+                                int64_t k_out_stride, void* stream);
+
+/*
+ * The 4-bit paged KV cache.  A page holds block_size tokens of one KV head;
+ * block b of the pool is the pages of all KV heads for block_size tokens.
+ *   pool   DEVICE uint8 [num_blocks][num_kv_heads][page_bytes], 16-byte
+ *          aligned, page_bytes = block_size * head_dim * 9 / 8:
+ *          K codes [block_size][d/2], K scales bf16 [block_size][d/32],
+ *          V codes and V scales alike
+ *   value  code * scale: code is e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their
+ *          negatives, sign in bit 3), one scale per 32 dimensions.  A row is
+ *          written with scale = bf16(max|x| / 6) and code = x / scale to the
+ *          nearest, ties to the even code, at most 6.  A group whose scale
+ *          would be below 2^-126 is written as zeros, one that holds an
+ *          infinity or a NaN gets a NaN scale.
+ *   codes  low nibble first, the pair of dimensions (i, i + 1), i even, at
+ *          byte (K) c * d/8 + 2 s + h, i = 16 s + 4 c + 2 h, c, h < (4, 2);
+ *               (V) r * d/16 + 2 g + h, i = 32 g + 4 r + 2 h, r, h < (8, 2)
+ *   slot   of a token: block * block_size + offset in the block
+ * block_size is 16, 32, 64, 128 or 256; num_blocks * block_size < 2^31.
+ */
+typedef struct waits_q4_cache {
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;         /* 64 or 128 */
+  void* pool;               /* DEVICE, waits_q4_pool_size() bytes */
+} waits_q4_cache;
+
+/* Bytes of `cache`'s pool (cache->pool is not looked at).  Host-only.
+ * Errors: ARG, SHAPE, UNSUPPORTED. */
+waits_status waits_q4_pool_size(const waits_q4_cache* cache, size_t* bytes);
+
+/*
+ * Block tables and slot maps from request lengths, on the device: gives
+ * sequence s the blocks it needs for new_len[s] more tokens.  With
+ * have = ceil(cache_len / block_size), want = ceil((cache_len + new_len) /
+ * block_size), sequences are served in order, and the k-th block handed out
+ * is free_list[free_count - 1 - k]; it becomes the table's next entry.
+ *   new_len     DEVICE int32 [nseq], >= 0
+ *   cache_len   DEVICE int32 [nseq]: tokens each sequence holds
+ *   block_table DEVICE int32 [nseq, max_blocks]: entries [0, have) are read
+ *               (of a block that is partly filled), entries [have, want) written
+ *   free_list   DEVICE int32 [num_blocks]: a stack of free blocks, read
+ *   free_count  DEVICE int32 [1]: blocks on the stack
+ *   cache_len_out, free_count_out  DEVICE: lengths and count afterwards; may
+ *               be cache_len and free_count themselves
+ *   slot_map    DEVICE int32 [max_new] or NULL: the slots of all new tokens,
+ *               sequence after sequence, then -1 up to max_new
+ *   cu_new      DEVICE int32 [nseq + 1] or NULL: where each sequence's new
+ *               tokens start in slot_map
+ *   status      DEVICE uint32 or NULL: WAITS_DEV_* bits are OR-ed in
+ * A sequence is refused, with its length and table kept and -1 slots, where
+ * the blocks left, its table row or slot_map are too small for it
+ * (WAITS_DEV_CACHE_FULL), or its cache_len or new_len is negative
+ * (WAITS_DEV_BAD_SEQLENS; a negative new_len counts as 0).  Once the free
+ * blocks did not suffice, later sequences that need any get none either.
+ * Blocks outside [0, num_blocks) in the table or the list give -1 slots and
+ * WAITS_DEV_BAD_INDEX.  nseq at most 8192.
+ * Errors: ARG, SHAPE, UNSUPPORTED, CUDA.
+ */
+waits_status waits_cache_reserve(int32_t nseq, int32_t block_size, int32_t max_blocks,
+                                 int32_t num_blocks, int32_t max_new, const int32_t* new_len,
+                                 const int32_t* cache_len, int32_t* block_table,
+                                 const int32_t* free_list, const int32_t* free_count,
+                                 int32_t* cache_len_out, int32_t* free_count_out,
+                                 int32_t* slot_map, int32_t* cu_new, uint32_t* status,
+                                 void* stream);
+
+/*
+ * Gives the blocks of ended sequences back: for each s with ended[s] != 0,
+ * in order, the ceil(cache_len[s] / block_size) blocks of its table row are
+ * pushed on the free list, the row's entries become -1 and cache_len[s] 0.
+ *   ended  DEVICE int32 [nseq]; other arguments as waits_cache_reserve
+ * Blocks outside [0, num_blocks), or more than the list has room for, are
+ * dropped with WAITS_DEV_BAD_INDEX; a length past the row is cut to it, and
+ * a negative one counts as 0, with WAITS_DEV_BAD_SEQLENS.  A block that two
+ * rows share is pushed by each: blocks have one owner here.
+ * Errors: ARG, SHAPE, UNSUPPORTED, CUDA.
+ */
+waits_status waits_cache_release(int32_t nseq, int32_t block_size, int32_t max_blocks,
+                                 int32_t num_blocks, const int32_t* ended, int32_t* cache_len,
+                                 int32_t* block_table, int32_t* free_list, int32_t* free_count,
+                                 uint32_t* status, void* stream);
+
+/*
+ * Quantises num_rows rows of K and V (all KV heads) into the cache's slots.
+ *   K, V      DEVICE bf16, row i's head g at K + i * k_stride + g * d
+ *             (strides in elements, multiples of 8), 16-byte aligned
+ *   slot_map  DEVICE int32 [num_rows]; a negative slot's row is skipped, one
+ *             past the pool too, with WAITS_DEV_BAD_INDEX.  Slots of a call
+ *             should differ: one given twice holds a mixture of its rows.
+ *   status    DEVICE uint32 or NULL: WAITS_DEV_* bits are OR-ed in
+ * Errors: ARG, SHAPE, UNSUPPORTED, CUDA.
+ */
+waits_status waits_q4_append(const waits_q4_cache* cache, int32_t num_rows, const void* K,
+                             int64_t k_stride, const void* V, int64_t v_stride,
+                             const int32_t* slot_map, uint32_t* status, void* stream);
+
+/*
+ * Reads slots back: K_out, V_out bf16 [num_rows, Hkv, d] = code * scale,
+ * rounded once; rows of negative slots, and of slots past the pool (which
+ * set WAITS_DEV_BAD_INDEX), are zero.  Arguments as waits_q4_append.
+ */
+waits_status waits_q4_read(const waits_q4_cache* cache, int32_t num_rows,
+                           const int32_t* slot_map, void* K_out, void* V_out,
+                           uint32_t* status, void* stream);
+
+/*
+ * waits_compact into the 4-bit paged cache: for j < kept_len[i] the row
+ * K[cu[i] + idx[i, g, j], g] is quantised into head g of slot
+ * block_table[i, j / block_size] * block_size + j % block_size; same for V.
+ * Nothing else of the pool is written.
+ *   shape, K, V, idx, kept_len, B  as waits_compact
+ *   block_table  DEVICE int32 [nseq, max_blocks], max_blocks * block_size >= B
+ *   status       DEVICE uint32 or NULL
+ * Rows whose idx or block is out of range are skipped and set
+ * WAITS_DEV_BAD_INDEX.
+ * Errors: ARG, SHAPE (heads or head_dim other than the cache's, a table
+ * narrower than B), UNSUPPORTED, CUDA.
+ */
+waits_status waits_q4_compact(const waits_shape* shape, const void* K, const void* V,
+                              const int32_t* idx, const int32_t* kept_len, int32_t B,
+                              const waits_q4_cache* cache, const int32_t* block_table,
+                              int32_t max_blocks, uint32_t* status, void* stream);
+
+/* Bytes of device workspace waits_q4_decode_attention needs.  Host-only. */
+waits_status waits_q4_decode_workspace_size(const waits_q4_cache* cache, int32_t nseq,
+                                            int32_t num_q_heads, size_t* bytes);
+
+/*
+ * waits_decode_attention over the 4-bit paged cache.  For sequence s and
+ * query head h, KV head g = h / G, over the slots j < cache_len[s] that the
+ * sequence's table row names:
+ *   out[s, h] = sum_j softmax_j(q[s, h] . K_j / sqrt(d)) * V_j
+ *   lse[s, h] = natural log of that softmax's normaliser (-inf, and out = 0,
+ *               for an empty cache)
+ * Codes enter the products exactly; scales, softmax and sums are fp32; the
+ * probabilities (times V's scale) are rounded to fp16 with a common power of
+ * two that keeps them in range.
+ *   q           DEVICE bf16 [nseq, Hq, d], 16-byte aligned
+ *   block_table DEVICE int32 [nseq, max_blocks]
+ *   cache_len   DEVICE int32 [nseq], clamped to [0, max_blocks * block_size]
+ *   out         DEVICE bf16 [nseq, Hq, d];  lse  DEVICE fp32 [nseq, Hq] or NULL
+ *   workspace   >= waits_q4_decode_workspace_size() bytes, 16-byte aligned;
+ *               calls that overlap on the GPU need one each
+ *   status      DEVICE uint32 or NULL
+ * Tokens of a table entry outside [0, num_blocks) are left out and set
+ * WAITS_DEV_BAD_INDEX.  Hq / Hkv at most 16, nseq at most 8192.
+ * Errors: ARG, SHAPE, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+waits_status waits_q4_decode_attention(const waits_q4_cache* cache, int32_t nseq,
+                                       int32_t num_q_heads, int32_t max_blocks, const void* q,
+                                       const int32_t* block_table, const int32_t* cache_len,
+                                       void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, uint32_t* status, void* stream);
 
 /*
  * Testing aid, no counterpart on the WAITS pages: y[i] = the scorer's

@@ -18,6 +18,7 @@ STATUS_NAMES = {0: "WAITS_OK", 1: "WAITS_ERR_ARG", 2: "WAITS_ERR_SHAPE",
                 5: "WAITS_ERR_CUDA", 6: "WAITS_ERR_TIMEOUT",
                 7: "WAITS_ERR_DEVICE"}
 DEV_TIMEOUT, DEV_BAD_SEQLENS, DEV_PLAN_OVERFLOW, DEV_BAD_INDEX, DEV_BAD_CURVE = 1, 2, 4, 8, 16
+DEV_CACHE_FULL = 32
 
 
 class WaitsLibraryError(RuntimeError):
@@ -45,11 +46,19 @@ class DeviceBuffers(ctypes.Structure):
                 ("cu_seqlens", ctypes.c_void_p)]
 
 
+class Q4Cache(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("pool", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
 _PSHAPE = ctypes.POINTER(Shape)
+_PCACHE = ctypes.POINTER(Q4Cache)
 
 # name -> (restype, argtypes); mirrors include/waits.h
 SIGNATURES = {
@@ -81,6 +90,17 @@ SIGNATURES = {
     "waits_decode_attention": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "waits_score_kernels": (_I, [_PSHAPE, _F, _I, ctypes.POINTER(ctypes.c_int32)]),
     "waits_select_compact": (_I, [_PSHAPE, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "waits_qk_norm_rope": (_I, [_I, _I, _I, _I, _I, _I, _P, _L, _P, _L, _P, _P, _P, _P, _F,
+                                _P, _L, _P, _L, _P]),
+    "waits_q4_pool_size": (_I, [_PCACHE, ctypes.POINTER(_SZ)]),
+    "waits_cache_reserve": (_I, [_I, _I, _I, _I, _I] + [_P] * 11),
+    "waits_cache_release": (_I, [_I, _I, _I, _I] + [_P] * 7),
+    "waits_q4_append": (_I, [_PCACHE, _I, _P, _L, _P, _L, _P, _P, _P]),
+    "waits_q4_read": (_I, [_PCACHE, _I, _P, _P, _P, _P, _P]),
+    "waits_q4_compact": (_I, [_PSHAPE, _P, _P, _P, _P, _I, _PCACHE, _P, _I, _P, _P]),
+    "waits_q4_decode_workspace_size": (_I, [_PCACHE, _I, _I, ctypes.POINTER(_SZ)]),
+    "waits_q4_decode_attention": (_I, [_PCACHE, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P,
+                                       _P]),
 }
 
 STATIC_WORKSPACE_BYTES = 32 << 20   # WAITS_STATIC_WORKSPACE_BYTES

@@ -15,6 +15,9 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
+from .cache import (  # noqa: F401
+    Q4Cache, cache_release, cache_reserve, q4_append, q4_compact, q4_decode_attention,
+    q4_decode_workspace_bytes, q4_page_bytes, q4_read, qk_norm_rope, rotary_inv_freq)
 
 
 def _ptr(t: Optional[torch.Tensor]):

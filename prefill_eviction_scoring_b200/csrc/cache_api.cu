@@ -1,0 +1,258 @@
+// C ABI of the operators around the 4-bit paged cache (head norms with
+// rotation, block tables, rows, compaction, decode attention): host-side
+// validation and launches.  Declarations and contracts: include/waits.h.
+#include <cmath>
+
+#include "waits_internal.cuh"
+
+using namespace waits;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// log2 of a supported block size, -1 otherwise
+int log_block(int32_t bs) {
+  for (int l = 4; l <= 8; ++l)
+    if (bs == 1 << l) return l;
+  return -1;
+}
+
+waits_status check_cache(const waits_q4_cache* c, Q4Pool* p) {
+  if (!c) return WAITS_ERR_ARG;
+  if (c->num_blocks < 1 || c->num_kv_heads < 1) return WAITS_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128) return WAITS_ERR_UNSUPPORTED;
+  const int lb = log_block(c->block_size);
+  if (lb < 0) return WAITS_ERR_UNSUPPORTED;
+  if (((int64_t)c->num_blocks << lb) > 0x7fffffffLL || c->num_kv_heads > 65535)
+    return WAITS_ERR_SHAPE;
+  *p = Q4Pool{static_cast<uint8_t*>(c->pool), c->num_blocks, lb, c->num_kv_heads, c->head_dim};
+  return WAITS_OK;
+}
+
+waits_status check_pool(const waits_q4_cache* c, Q4Pool* p) {
+  const waits_status st = check_cache(c, p);
+  if (st == WAITS_OK && (!c->pool || !aligned(c->pool, 16))) return WAITS_ERR_ARG;
+  return st;
+}
+
+bool stride_ok(int64_t stride, int64_t heads, int64_t d) {
+  return stride % 8 == 0 && stride >= heads * d && stride <= (int64_t)1 << 40;
+}
+
+waits_status check_tables(int32_t nseq, int32_t block_size, int32_t max_blocks,
+                          int32_t num_blocks, int* log_bs) {
+  if (nseq < 1 || max_blocks < 1 || num_blocks < 1) return WAITS_ERR_SHAPE;
+  *log_bs = log_block(block_size);
+  if (*log_bs < 0 || nseq > kMaxReserveSeqs) return WAITS_ERR_UNSUPPORTED;
+  if (((int64_t)num_blocks << *log_bs) > 0x7fffffffLL ||
+      ((int64_t)max_blocks << *log_bs) > 0x7fffffffLL)
+    return WAITS_ERR_SHAPE;
+  return WAITS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+waits_status waits_qk_norm_rope(int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                                const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const int32_t* positions, const double* inv_freq,
+                                const void* q_weight, const void* k_weight, float eps,
+                                void* q_out, int64_t q_out_stride, void* k_out,
+                                int64_t k_out_stride, void* stream) {
+  if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads > 65535 ||
+      num_kv_heads > 65535)
+    return WAITS_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return WAITS_ERR_UNSUPPORTED;
+  if (rotary_dim < 8 || rotary_dim > head_dim || rotary_dim % 8) return WAITS_ERR_SHAPE;
+  if (!inv_freq || !std::isfinite(eps) || eps < 0.0f) return WAITS_ERR_ARG;
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    if (!std::isfinite(inv_freq[i])) return WAITS_ERR_ARG;
+  if ((q_weight == nullptr) != (k_weight == nullptr)) return WAITS_ERR_ARG;
+  if (!stride_ok(q_stride, num_q_heads, head_dim) ||
+      !stride_ok(k_stride, num_kv_heads, head_dim) ||
+      !stride_ok(q_out_stride, num_q_heads, head_dim) ||
+      !stride_ok(k_out_stride, num_kv_heads, head_dim))
+    return WAITS_ERR_ARG;
+  if (num_tokens == 0) return WAITS_OK;
+  if (!q || !k || !q_out || !k_out || !positions) return WAITS_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4))
+    return WAITS_ERR_ARG;
+  if ((q == q_out && q_stride != q_out_stride) || (k == k_out && k_stride != k_out_stride))
+    return WAITS_ERR_ARG;
+  RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.qw = static_cast<const uint16_t*>(q_weight);
+  a.kw = static_cast<const uint16_t*>(k_weight);
+  a.qo = static_cast<uint16_t*>(q_out);
+  a.ko = static_cast<uint16_t*>(k_out);
+  a.qs = q_stride;
+  a.ks = k_stride;
+  a.qos = q_out_stride;
+  a.kos = k_out_stride;
+  a.pos = positions;
+  a.T = num_tokens;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.d = head_dim;
+  a.rot = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.eps = eps;
+  a.inv_freq = inv_freq;
+  const cudaError_t err = launch_rope(a, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("norm and rotation launch", err);
+}
+
+waits_status waits_q4_pool_size(const waits_q4_cache* cache, size_t* bytes) {
+  if (!bytes) return WAITS_ERR_ARG;
+  Q4Pool p;
+  const waits_status st = check_cache(cache, &p);
+  if (st != WAITS_OK) return st;
+  *bytes = ((size_t)p.num_blocks << p.log_bs) * p.Hkv * p.d / 8 * 9;
+  return WAITS_OK;
+}
+
+waits_status waits_cache_reserve(int32_t nseq, int32_t block_size, int32_t max_blocks,
+                                 int32_t num_blocks, int32_t max_new, const int32_t* new_len,
+                                 const int32_t* cache_len, int32_t* block_table,
+                                 const int32_t* free_list, const int32_t* free_count,
+                                 int32_t* cache_len_out, int32_t* free_count_out,
+                                 int32_t* slot_map, int32_t* cu_new, uint32_t* status,
+                                 void* stream) {
+  int lb;
+  const waits_status st = check_tables(nseq, block_size, max_blocks, num_blocks, &lb);
+  if (st != WAITS_OK) return st;
+  if (max_new < 0) return WAITS_ERR_SHAPE;
+  if (!new_len || !cache_len || !block_table || !free_list || !free_count || !cache_len_out ||
+      !free_count_out)
+    return WAITS_ERR_ARG;
+  for (const void* p : {(const void*)new_len, (const void*)cache_len, (const void*)block_table,
+                        (const void*)free_list, (const void*)free_count,
+                        (const void*)cache_len_out, (const void*)free_count_out,
+                        (const void*)slot_map, (const void*)cu_new, (const void*)status})
+    if (!aligned(p, 4)) return WAITS_ERR_ARG;
+  const ReserveArgs a{nseq,       lb,        max_blocks,    num_blocks,     max_new,
+                      new_len,    cache_len, block_table,   free_list,      free_count,
+                      cache_len_out, free_count_out, slot_map, cu_new, status};
+  const cudaError_t err = launch_reserve(a, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("reserve launch", err);
+}
+
+waits_status waits_cache_release(int32_t nseq, int32_t block_size, int32_t max_blocks,
+                                 int32_t num_blocks, const int32_t* ended, int32_t* cache_len,
+                                 int32_t* block_table, int32_t* free_list, int32_t* free_count,
+                                 uint32_t* status, void* stream) {
+  int lb;
+  const waits_status st = check_tables(nseq, block_size, max_blocks, num_blocks, &lb);
+  if (st != WAITS_OK) return st;
+  if (!ended || !cache_len || !block_table || !free_list || !free_count) return WAITS_ERR_ARG;
+  for (const void* p : {(const void*)ended, (const void*)cache_len, (const void*)block_table,
+                        (const void*)free_list, (const void*)free_count, (const void*)status})
+    if (!aligned(p, 4)) return WAITS_ERR_ARG;
+  const cudaError_t err = launch_release(nseq, lb, max_blocks, num_blocks, ended, cache_len,
+                                         block_table, free_list, free_count, status,
+                                         static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("release launch", err);
+}
+
+waits_status waits_q4_append(const waits_q4_cache* cache, int32_t num_rows, const void* K,
+                             int64_t k_stride, const void* V, int64_t v_stride,
+                             const int32_t* slot_map, uint32_t* status, void* stream) {
+  Q4Pool p;
+  const waits_status st = check_pool(cache, &p);
+  if (st != WAITS_OK) return st;
+  if (num_rows < 0) return WAITS_ERR_SHAPE;
+  if (!stride_ok(k_stride, p.Hkv, p.d) || !stride_ok(v_stride, p.Hkv, p.d)) return WAITS_ERR_ARG;
+  if (num_rows == 0) return WAITS_OK;
+  if (!K || !V || !slot_map || !aligned(K, 16) || !aligned(V, 16) || !aligned(slot_map, 4) ||
+      !aligned(status, 4))
+    return WAITS_ERR_ARG;
+  const cudaError_t err = launch_q4_append(
+      p, num_rows, static_cast<const uint16_t*>(K), k_stride, static_cast<const uint16_t*>(V),
+      v_stride, slot_map, status, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("4-bit append launch", err);
+}
+
+waits_status waits_q4_read(const waits_q4_cache* cache, int32_t num_rows,
+                           const int32_t* slot_map, void* K_out, void* V_out, uint32_t* status,
+                           void* stream) {
+  Q4Pool p;
+  const waits_status st = check_pool(cache, &p);
+  if (st != WAITS_OK) return st;
+  if (num_rows < 0) return WAITS_ERR_SHAPE;
+  if (num_rows == 0) return WAITS_OK;
+  if (!K_out || !V_out || !slot_map || !aligned(K_out, 16) || !aligned(V_out, 16) ||
+      !aligned(slot_map, 4) || !aligned(status, 4))
+    return WAITS_ERR_ARG;
+  const cudaError_t err =
+      launch_q4_read(p, num_rows, slot_map, static_cast<uint16_t*>(K_out),
+                     static_cast<uint16_t*>(V_out), status, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("4-bit read launch", err);
+}
+
+waits_status waits_q4_compact(const waits_shape* shape, const void* K, const void* V,
+                              const int32_t* idx, const int32_t* kept_len, int32_t B,
+                              const waits_q4_cache* cache, const int32_t* block_table,
+                              int32_t max_blocks, uint32_t* status, void* stream) {
+  Q4Pool p;
+  size_t bytes;
+  waits_status st = waits_workspace_size(shape, &bytes);   // the shape's own checks
+  if (st == WAITS_OK) st = check_pool(cache, &p);
+  if (st != WAITS_OK) return st;
+  if (shape->num_kv_heads != p.Hkv || shape->head_dim != p.d) return WAITS_ERR_SHAPE;
+  if (B < 1) return WAITS_ERR_ARG;
+  if (max_blocks < 1 || ((int64_t)max_blocks << p.log_bs) < B) return WAITS_ERR_SHAPE;
+  if (!K || !V || !idx || !kept_len || !block_table || !aligned(K, 16) || !aligned(V, 16) ||
+      !aligned(idx, 4) || !aligned(kept_len, 4) || !aligned(block_table, 4) || !aligned(status, 4))
+    return WAITS_ERR_ARG;
+  const cudaError_t err = launch_q4_compact(
+      p, static_cast<const uint16_t*>(K), static_cast<const uint16_t*>(V), shape->cu_seqlens, idx,
+      kept_len, shape->nseq, shape->total_tokens, B, block_table, max_blocks, status,
+      static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("4-bit compaction launch", err);
+}
+
+static waits_status check_q4_decode(const Q4Pool& p, int32_t nseq, int32_t Hq) {
+  if (nseq < 1 || Hq < 1 || Hq % p.Hkv || Hq > 65535) return WAITS_ERR_SHAPE;
+  if (Hq / p.Hkv > 16 || nseq > kMaxReserveSeqs) return WAITS_ERR_UNSUPPORTED;
+  return WAITS_OK;
+}
+
+waits_status waits_q4_decode_workspace_size(const waits_q4_cache* cache, int32_t nseq,
+                                            int32_t num_q_heads, size_t* bytes) {
+  if (!bytes) return WAITS_ERR_ARG;
+  Q4Pool p;
+  waits_status st = check_cache(cache, &p);
+  if (st == WAITS_OK) st = check_q4_decode(p, nseq, num_q_heads);
+  if (st != WAITS_OK) return st;
+  *bytes = q4_decode_workspace_bytes(p, nseq, num_q_heads);
+  return WAITS_OK;
+}
+
+waits_status waits_q4_decode_attention(const waits_q4_cache* cache, int32_t nseq,
+                                       int32_t num_q_heads, int32_t max_blocks, const void* q,
+                                       const int32_t* block_table, const int32_t* cache_len,
+                                       void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, uint32_t* status, void* stream) {
+  Q4Pool p;
+  waits_status st = check_pool(cache, &p);
+  if (st == WAITS_OK) st = check_q4_decode(p, nseq, num_q_heads);
+  if (st != WAITS_OK) return st;
+  if (max_blocks < 1 || ((int64_t)max_blocks << p.log_bs) > 0x7fffffffLL) return WAITS_ERR_SHAPE;
+  if (!q || !block_table || !cache_len || !out || !aligned(q, 16) || !aligned(block_table, 4) ||
+      !aligned(cache_len, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(status, 4))
+    return WAITS_ERR_ARG;
+  if (!workspace || !aligned(workspace, 16) ||
+      workspace_bytes < q4_decode_workspace_bytes(p, nseq, num_q_heads))
+    return WAITS_ERR_WORKSPACE;
+  const cudaError_t err = launch_q4_decode(
+      p, nseq, num_q_heads, max_blocks, static_cast<const uint16_t*>(q), block_table, cache_len,
+      static_cast<uint16_t*>(out), lse, workspace, status, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? WAITS_OK : report_cuda("4-bit decode launch", err);
+}
+
+}  // extern "C"

@@ -244,6 +244,8 @@ waits_status check_compact_args(const void* K, const void* V, const int32_t* idx
 }  // namespace
 
 namespace waits {
+waits_status report_cuda(const char* what, cudaError_t err) { return cuda_fail(what, err); }
+
 void set_error_detail(const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

@@ -312,6 +312,9 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 // Extra text appended to the next waits_last_error() message (host only).
 void set_error_detail(const char* fmt, ...);
 
+// Records a CUDA failure for waits_last_error and returns WAITS_ERR_CUDA.
+waits_status report_cuda(const char* what, cudaError_t err);
+
 // Host-side launchers (one per translation unit).
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s);
 struct HostPlan;
@@ -345,5 +348,54 @@ int decode_max_group();
 cudaError_t launch_decode(int nseq, int Hq, int Hkv, int d, int C, const uint16_t* q,
                           const uint16_t* Kc, const uint16_t* Vc, const int32_t* len, float* out,
                           float* lse, float* part, cudaStream_t st);
+
+// Head norms with rotary positions (rope.cu).
+struct RopeArgs {
+  const uint16_t *q, *k, *qw, *kw;
+  uint16_t *qo, *ko;
+  int64_t qs, ks, qos, kos;   // token strides, elements
+  const int32_t* pos;
+  int T, Hq, Hkv, d, rot;
+  bool interleaved;
+  float eps;
+  const double* inv_freq;     // host
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+
+// Block tables and slot maps (paged.cu).
+constexpr int kMaxReserveSeqs = 8192;
+struct ReserveArgs {
+  int nseq, log_bs, width, num_blocks, max_new;
+  const int32_t *new_len, *cache_len;
+  int32_t* table;
+  const int32_t *free_list, *free_count;
+  int32_t *len_out, *count_out, *slots, *cu_new;
+  uint32_t* status;
+};
+cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t st);
+cudaError_t launch_release(int nseq, int log_bs, int width, int num_blocks, const int32_t* ended,
+                           int32_t* len, int32_t* table, int32_t* free_list, int32_t* free_count,
+                           uint32_t* status, cudaStream_t st);
+
+// Rows into and out of the 4-bit paged cache (q4_rows.cu).
+struct Q4Pool {
+  uint8_t* pool;
+  int num_blocks, log_bs, Hkv, d;
+};
+cudaError_t launch_q4_append(const Q4Pool& c, int n, const uint16_t* K, int64_t ks,
+                             const uint16_t* V, int64_t vs, const int32_t* slots,
+                             uint32_t* status, cudaStream_t st);
+cudaError_t launch_q4_read(const Q4Pool& c, int n, const int32_t* slots, uint16_t* K, uint16_t* V,
+                           uint32_t* status, cudaStream_t st);
+cudaError_t launch_q4_compact(const Q4Pool& c, const uint16_t* K, const uint16_t* V,
+                              const int32_t* cu, const int32_t* idx, const int32_t* kept_len,
+                              int nseq, int T, int B, const int32_t* table, int width,
+                              uint32_t* status, cudaStream_t st);
+
+// Decode attention over the 4-bit paged cache (q4_attention.cu).
+size_t q4_decode_workspace_bytes(const Q4Pool& c, int nseq, int Hq);
+cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const uint16_t* q,
+                             const int32_t* table, const int32_t* len, uint16_t* out, float* lse,
+                             void* ws, uint32_t* status, cudaStream_t st);
 
 }  // namespace waits

@@ -1,0 +1,171 @@
+"""Host-side checks of the operators around the 4-bit paged cache: the C
+entries reject bad arguments before any CUDA call, the Python ones reject
+tensors they cannot take."""
+
+import ctypes
+
+import pytest
+import torch
+
+import prefill_eviction_scoring_b200 as pkg
+from prefill_eviction_scoring_b200 import _lib, api, build
+
+P = 0x100000        # never dereferenced: every call below fails validation, or does nothing
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def _cache(**kw):
+    d = dict(num_blocks=10, block_size=16, num_kv_heads=2, head_dim=128, pool=P)
+    d.update(kw)
+    return _lib.Q4Cache(**d)
+
+
+def _rope(lib, n=4, Hq=8, Hkv=2, d=128, rot=128, q=P, qs=1024, k=P, ks=256, pos=P, inv=None,
+          qw=None, kw=None, eps=1e-6, qo=P, qos=1024, ko=P, kos=256, freq=1.0):
+    f = (ctypes.c_double * 64)(*[freq] * 64)
+    return lib.waits_qk_norm_rope(n, Hq, Hkv, d, rot, 0, q, qs, k, ks, pos,
+                                  None if inv == 0 else ctypes.cast(f, ctypes.c_void_p), qw, kw,
+                                  eps, qo, qos, ko, kos, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), 2), (dict(Hq=0), 2), (dict(Hkv=0), 2), (dict(d=96), 3), (dict(d=256), 3),
+    (dict(rot=0), 2), (dict(rot=12), 2), (dict(rot=136), 2), (dict(rot=-8), 2),
+    (dict(q=None), 1), (dict(k=None), 1), (dict(pos=None), 1), (dict(inv=0), 1),
+    (dict(qo=None), 1), (dict(ko=None), 1), (dict(q=P + 8), 1), (dict(ko=P + 2), 1),
+    (dict(qs=1020), 1), (dict(qs=1016), 1), (dict(ks=128), 1), (dict(ks=260), 1), (dict(ks=-256), 1),
+    (dict(qw=P), 1), (dict(kw=P), 1), (dict(qw=P, kw=P + 4), 1),
+    (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
+    (dict(freq=float("nan")), 1), (dict(freq=float("inf")), 1),
+    (dict(qos=2048), 1), (dict(kos=512), 1),          # in place with another stride
+    (dict(n=0, q=None, k=None, qo=None, ko=None, pos=None), 0)])
+def test_rope_arguments(lib, kw, want):
+    assert _rope(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(num_blocks=0), 2), (dict(num_kv_heads=0), 2), (dict(head_dim=96), 3),
+    (dict(block_size=8), 3), (dict(block_size=48), 3), (dict(block_size=512), 3),
+    (dict(num_blocks=1 << 27), 2), (dict(), 0)])
+def test_pool_size(lib, kw, want):
+    n = ctypes.c_size_t(0)
+    assert lib.waits_q4_pool_size(ctypes.byref(_cache(**kw)), ctypes.byref(n)) == want
+    if want == 0:
+        assert n.value == 10 * 2 * 16 * 144
+    assert lib.waits_q4_pool_size(None, ctypes.byref(n)) == 1
+    assert lib.waits_q4_pool_size(ctypes.byref(_cache()), None) == 1
+
+
+def test_reserve_and_release_arguments(lib):
+    good = dict(nseq=4, bs=16, width=5, blocks=20, new=64)
+
+    def reserve(ptrs=(P,) * 11, **kw):
+        a = {**good, **kw}
+        return lib.waits_cache_reserve(a["nseq"], a["bs"], a["width"], a["blocks"], a["new"],
+                                       *ptrs[:10], None)
+
+    for kw, want in ((dict(nseq=0), 2), (dict(nseq=8193), 3), (dict(bs=0), 3), (dict(bs=24), 3),
+                     (dict(width=0), 2), (dict(blocks=0), 2), (dict(new=-1), 2),
+                     (dict(width=1 << 28), 2), (dict(blocks=1 << 28), 2)):
+        assert reserve(**kw) == want, kw
+    for i in range(7):                                # slot_map, cu_new, status may be NULL
+        ptrs = [P] * 11
+        ptrs[i] = None
+        assert reserve(ptrs) == 1, i
+    for i in range(10):
+        ptrs = [P] * 11
+        ptrs[i] = P + 2
+        assert reserve(ptrs) == 1, i
+
+    def release(ptrs=(P,) * 6, nseq=4, bs=16, width=5, blocks=20):
+        return lib.waits_cache_release(nseq, bs, width, blocks, *ptrs, None)
+
+    assert release(nseq=0) == 2 and release(nseq=8193) == 3 and release(bs=17) == 3
+    for i in range(5):
+        ptrs = [P] * 6
+        ptrs[i] = None
+        assert release(ptrs) == 1, i
+
+
+def test_row_arguments(lib):
+    c = _cache()
+    append = lambda c=c, n=3, K=P, ks=256, V=P, vs=256, s=P, st=None: lib.waits_q4_append(
+        ctypes.byref(c), n, K, ks, V, vs, s, st, None)
+    assert append(n=-1) == 2 and append(K=None) == 1 and append(V=P + 8) == 1
+    assert append(ks=248) == 1 and append(vs=260) == 1 and append(s=None) == 1
+    assert append(c=_cache(pool=None)) == 1 and append(c=_cache(pool=P + 8)) == 1
+    assert append(c=_cache(head_dim=32)) == 3 and append(st=P + 1) == 1
+    assert append(n=0, K=None, V=None, s=None) == 0
+    read = lambda c=c, n=3, s=P, K=P, V=P: lib.waits_q4_read(ctypes.byref(c), n, s, K, V, None,
+                                                             None)
+    assert read(n=-1) == 2 and read(K=None) == 1 and read(V=P + 4) == 1 and read(s=None) == 1
+    assert read(n=0, s=None, K=None, V=None) == 0
+    sh = _lib.Shape(2, 100, 100, 2, 2, 128, P)
+
+    def compact(sh=sh, K=P, V=P, idx=P, kept=P, B=40, c=c, table=P, width=3):
+        return lib.waits_q4_compact(ctypes.byref(sh), K, V, idx, kept, B, ctypes.byref(c), table,
+                                    width, None, None)
+
+    assert compact(K=None) == 1 and compact(idx=None) == 1 and compact(table=None) == 1
+    assert compact(B=0) == 1 and compact(width=2) == 2 and compact(width=0) == 2
+    assert compact(c=_cache(num_kv_heads=4)) == 2 and compact(c=_cache(head_dim=64)) == 2
+    assert compact(sh=_lib.Shape(0, 100, 100, 2, 2, 128, P)) == 2
+
+
+def test_attention_arguments(lib):
+    c = _cache()
+    n = ctypes.c_size_t(0)
+    assert lib.waits_q4_decode_workspace_size(ctypes.byref(c), 4, 8, ctypes.byref(n)) == 0
+    ws = n.value
+    assert ws >= 1
+    size = lambda c=c, nseq=4, Hq=8: lib.waits_q4_decode_workspace_size(
+        ctypes.byref(c), nseq, Hq, ctypes.byref(n))
+    assert size(nseq=0) == 2 and size(Hq=7) == 2 and size(Hq=34) == 3 and size(nseq=8193) == 3
+    assert lib.waits_q4_decode_workspace_size(ctypes.byref(c), 4, 8, None) == 1
+
+    def attend(c=c, nseq=4, Hq=8, width=3, q=P, table=P, length=P, out=P, lse=None, w=P, nb=ws,
+               st=None):
+        return lib.waits_q4_decode_attention(ctypes.byref(c), nseq, Hq, width, q, table, length,
+                                             out, lse, w, nb, st, None)
+
+    for kw, want in ((dict(q=None), 1), (dict(table=None), 1), (dict(length=None), 1),
+                     (dict(out=None), 1), (dict(out=P + 2), 1), (dict(q=P + 8), 1),
+                     (dict(lse=P + 2), 1), (dict(w=None), 4), (dict(w=P + 4), 4),
+                     (dict(nb=ws - 1), 4), (dict(width=0), 2), (dict(width=1 << 28), 2),
+                     (dict(Hq=9), 2), (dict(Hq=64), 3), (dict(c=_cache(pool=None)), 1)):
+        assert attend(**kw) == want, kw
+
+
+def test_python_refuses_what_it_cannot_take():
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    inv = api.rotary_inv_freq(64, 10000.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.qk_norm_rope(q, q, i, inv)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.cache_reserve(i, i, i.view(1, 2), i, i[:1], block_size=16, max_new=2)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.cache_release(i, i, i.view(1, 2), i, i[:1], block_size=16)
+    pool = torch.zeros((2, 4, 16 * 72), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.q4_append(q, q, i, pool)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.q4_read(pool, i, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.q4_compact(q, q, i, i.view(1, 1, 2), i[:1], i.view(1, 2), pool)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.q4_decode_attention(q, pool, i.view(2, 1), i)
+
+
+def test_helpers():
+    assert torch.equal(api.rotary_inv_freq(8, 16.0),
+                       torch.tensor([1.0, 0.5, 0.25, 0.125], dtype=torch.float64))
+    assert api.q4_page_bytes(16, 128) == 2304 and api.q4_page_bytes(64, 64) == 4608
+    for name in ("Q4Cache", "qk_norm_rope", "cache_reserve", "cache_release", "q4_append",
+                 "q4_read", "q4_compact", "q4_decode_attention"):
+        assert getattr(pkg, name) is getattr(api, name)
