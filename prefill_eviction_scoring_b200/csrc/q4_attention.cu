@@ -1,116 +1,654 @@
 // One decode step of attention over the 4-bit paged cache.
 //
 // o[s, h] = sum_j softmax_j(q[s, h] . K_j / sqrt(d)) V_j, K_j and V_j = code *
-// scale.  A CTA takes one (sequence, KV head); its warps take the tokens in
-// turn, a lane the dimensions 4 l .. 4 l + 3, with a running maximum and sum
-// per head; the warps' results are merged in shared memory.
+// scale.  HBM bounds it: 1.125 d bytes per (token, KV head), read once for
+// all G query heads of the group.
+//
+// Split: the work is the list of all 16-token tiles of all (sequence, KV
+// head) items, and every CTA takes an equal run of it, whatever the lengths
+// (they are known on the device only).  A run covers whole items, whose
+// output it writes, and at most two parts of items, whose (weighted sum,
+// maximum, sum) go to the workspace; a second kernel joins the parts of an
+// item in order.  So the workspace depends on the grid alone and the result
+// on nothing but the inputs.
+//
+// A warp takes every eighth tile of its CTA's run: it streams the tile's
+// codes and scales into its own ring of shared memory (cp.async, kStages - 1
+// tiles ahead, across item boundaries), forms the logits and the weighted
+// sum with mma.m16n8k16 and keeps its own running maximum and sums; the
+// CTA's warps meet only at the end of an item.  tcgen05 would need the
+// decoded operands in shared memory, 3.5 bytes written for each byte read;
+// here the fragments are decoded in registers: the page's byte order makes
+// each lane's codes contiguous and in fragment order.
+//
+// Exactness: e2m1 codes are exact in fp16; q is scaled by a power of two
+// into fp16's range (exact above 2^-24 of its largest value); group sums are
+// scaled in fp32.  The weights p_j * scale_jg enter the second product in
+// fp16 (2^-11 relative; bf16 would give 2^-8), after a power of two per warp
+// and group keeps them below 2^14 and V's largest scale near 1.
 #include "q4.cuh"
 
 namespace waits {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMaxG = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTok = 16;              // tokens per tile
+constexpr int kStages = 4;
+constexpr int kCtasPerSm = 2;
+constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
+constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
+
+struct Desc {       // the item whose parts begin with this CTA's last one
+  int32_t s, g, parts, slot;
+};
+
+struct DecodeArgs {
+  Q4Pool c;
+  int nseq, Hq, G, width;
+  const uint16_t* q;
+  const int32_t *table, *len;
+  uint16_t* out;
+  float *lse, *part;
+  Desc* desc;
+  uint32_t* status;
+  float scale_log2;
+};
+
+__device__ inline void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ inline uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ inline float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ inline uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ inline void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ inline void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ inline void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ inline int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32)
-    q4_decode_kernel(Q4Pool c, int Hq, int width, const uint16_t* __restrict__ q,
-                     const int32_t* __restrict__ table, const int32_t* __restrict__ len,
-                     uint16_t* __restrict__ out, float* __restrict__ lse, float scale_log2,
-                     uint32_t* status) {
-  constexpr int kE = D / 32;              // dimensions per lane
-  __shared__ float sm_m[kWarps][kMaxG], sm_l[kWarps][kMaxG];
-  __shared__ float sm_o[kWarps][D];
+struct Smem {
+  static constexpr int kTileBytes = kTok * D * 9 / 8;
+  static constexpr int kCodes = kTok * D / 2;           // bytes of one tile's K (or V) codes
+  static constexpr int kScales = kTok * D / 16;
+  static constexpr int kRow = D + 4;                    // floats per merge row, no bank conflicts
+  uint8_t ring[kWarps][kStages][kTileBytes];
+  float o[kWarps][8][kRow];
+  float m[kWarps][16], l[kWarps][16];
+  int32_t page_ok[kWarps][kStages];
+  int64_t scan[kWarps];
+  int64_t total;
+  int64_t where[2];                                     // sequence of the run's start, units before it
+};
+
+// The partial of a part: [G][D] weighted sums, then G maxima and G sums;
+// whole 16-byte vectors.
+__host__ __device__ inline size_t part_floats(int G, int D) {
+  return ((size_t)G * (D + 2) + 3) / 4 * 4;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const DecodeArgs a) {
+  constexpr int NG = D / 32, NW2 = D / 64;
+  using S = Smem<D>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int Hkv = a.c.Hkv, G = a.G, log_bs = a.c.log_bs;
+  const int64_t cap = (int64_t)a.width << log_bs;
+  const size_t page_bytes = Q4Page<D>::bytes(log_bs);
   pdl_allow_next();
   pdl_wait();
-  const int g = blockIdx.x, s = blockIdx.y;
-  const int G = Hq / c.Hkv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t cap = (int64_t)width << c.log_bs;
-  const int64_t n = len[s] < 0 ? 0 : (len[s] > cap ? cap : len[s]);
-  float qv[kMaxG][kE], o[kMaxG][kE], m[kMaxG], l[kMaxG];
-  for (int h = 0; h < G; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-    for (int e = 0; e < kE; ++e) {
-      o[h][e] = 0.f;
-      qv[h][e] = __uint_as_float(
-          (uint32_t)q[((int64_t)s * Hq + g * G + h) * D + kE * lane + e] << 16);
-    }
+
+  auto tokens = [&](int s) -> int {
+    const int64_t n = a.len[s];
+    return (int)(n < 0 ? 0 : (n > cap ? cap : n));
+  };
+  auto tiles = [&](int s) -> int { return (int)(((int64_t)tokens(s) + kTok - 1) / kTok); };
+
+  // empty sequences, shared among the CTAs
+  for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
+    if (tokens(s) > 0) continue;
+    for (int i = tid; i < a.Hq * D / 2; i += kThreads)
+      reinterpret_cast<uint32_t*>(a.out + (size_t)s * a.Hq * D)[i] = 0;
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)s * a.Hq + i] = -INFINITY;
   }
-  for (int64_t j = warp; j < n; j += kWarps) {
-    const int block = table[(int64_t)s * width + (j >> c.log_bs)];
-    if ((unsigned)block >= (unsigned)c.num_blocks) {
-      if (status && lane == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
-      continue;
-    }
-    const int off = (int)(j & ((1 << c.log_bs) - 1));
-    const uint8_t* page = c.pool + ((size_t)block * c.Hkv + g) * Q4Page<D>::bytes(c.log_bs);
-    const uint8_t* kr = page + Q4Page<D>::code(0, c.log_bs, off);
-    const uint8_t* vr = page + Q4Page<D>::code(1, c.log_bs, off);
-    float kf[kE], vf[kE];
-    for (int e = 0; e < kE; e += 2) {
-      const int i = kE * lane + e;
-      const uint32_t kb = kr[(i % 16 / 4) * (D / 8) + 2 * (i / 16) + (i % 4) / 2];
-      const uint32_t vb = vr[(i % 32 / 4) * (D / 16) + 2 * (i / 32) + (i % 4) / 2];
-      uint32_t h4[4];
-      e2m1_to_half(kb | (vb << 8), h4);
-      const uint16_t* ksc = reinterpret_cast<const uint16_t*>(page + Q4Page<D>::scale(0, c.log_bs, off));
-      const uint16_t* vsc = reinterpret_cast<const uint16_t*>(page + Q4Page<D>::scale(1, c.log_bs, off));
-      const float ks = __uint_as_float((uint32_t)ksc[i / 32] << 16);
-      const float vs = __uint_as_float((uint32_t)vsc[i / 32] << 16);
-      const float2 a = half2_to_float2(h4[0]), b = half2_to_float2(h4[1]);
-      kf[e] = a.x * ks;
-      kf[e + 1] = a.y * ks;
-      vf[e] = b.x * vs;
-      vf[e + 1] = b.y * vs;
-    }
-    for (int h = 0; h < G; ++h) {
-      float x = 0.f;
-      for (int e = 0; e < kE; ++e) x = fmaf(qv[h][e], kf[e], x);
-      for (int b = 16; b > 0; b >>= 1) x += __shfl_xor_sync(0xffffffffu, x, b);
-      x *= scale_log2;
-      const float top = fmaxf(m[h], x);
-      const float f = exp2f(m[h] - top), p = exp2f(x - top);
-      m[h] = top;
-      l[h] = l[h] * f + p;
-      for (int e = 0; e < kE; ++e) o[h][e] = o[h][e] * f + p * vf[e];
-    }
+
+  // total units (tiles of all items), then this CTA's run [u0, u1)
+  int64_t mine = 0;
+  for (int s = tid; s < a.nseq; s += kThreads) mine += tiles(s);
+  mine = warp_sum(mine);
+  if (lane == 0) sm.scan[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
+  total *= Hkv;
+  // one tile per warp at least
+  int64_t ctas = (total + kWarps - 1) / kWarps;
+  ctas = ctas < gridDim.x ? ctas : gridDim.x;
+  if (blockIdx.x >= ctas) {
+    if (tid == 0) a.desc[blockIdx.x].parts = 0;
+    return;
   }
-  for (int h = 0; h < G; ++h) {
+  const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+  // the sequence of u0: prefix sums, kThreads sequences at a time
+  {
+    int64_t before = 0;
+    for (int s0 = 0;; s0 += kThreads) {
+      const int s = s0 + tid;
+      const int64_t t = s < a.nseq ? (int64_t)tiles(s) * Hkv : 0;
+      int64_t x = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) sm.scan[warp] = x;
+      __syncthreads();
+      int64_t sum = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) x += sm.scan[w];
+        sum += sm.scan[w];
+      }
+      x += before;
+      if (t > 0 && x - t <= u0 && u0 < x) {
+        sm.where[0] = s;
+        sm.where[1] = x - t;
+      }
+      before += sum;
+      if (before > u0) break;
+    }
     __syncthreads();
-    if (lane == 0) {
-      sm_m[warp][h] = m[h];
-      sm_l[warp][h] = l[h];
-    }
-    for (int e = 0; e < kE; ++e) sm_o[warp][kE * lane + e] = o[h][e];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][h]);
-    const int64_t row = (int64_t)s * Hq + g * G + h;
-    for (int w = 0; w < kWarps; ++w) L += sm_l[w][h] > 0.f ? sm_l[w][h] * exp2f(sm_m[w][h] - M) : 0.f;
-    for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-      float a = 0.f;
-      for (int w = 0; w < kWarps; ++w)
-        if (sm_l[w][h] > 0.f) a += sm_o[w][i] * exp2f(sm_m[w][h] - M);
-      out[row * D + i] = (uint16_t)(pack_bf16(L > 0.f ? a / L : 0.f, 0.f) & 0xffffu);
-    }
-    if (lse && threadIdx.x == 0)
-      lse[row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
   }
+  int s = (int)sm.where[0], nt = tiles(s);
+  const int64_t in_seq = u0 - sm.where[1];
+  int g = (int)(in_seq / nt), tile0 = (int)(in_seq - (int64_t)g * nt);
+
+  // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..
+  int64_t p_left = (u1 - u0 - warp + kWarps - 1) / kWarps;   // tiles not yet issued
+  if (u1 - u0 <= warp) p_left = 0;
+  int p_s = s, p_g = g, p_nt = nt, p_tile = tile0, p_stage = 0, p_block = -1;
+  auto settle = [&]() {      // bring p_tile into its item; load its block
+    while (p_tile >= p_nt) {
+      p_tile -= p_nt;
+      if (++p_g == Hkv) {
+        p_g = 0;
+        do ++p_s; while ((p_nt = tiles(p_s)) == 0);
+      }
+    }
+    p_block = __ldg(a.table + (int64_t)p_s * a.width + (((int64_t)p_tile * kTok) >> log_bs));
+  };
+  if (p_left > 0) {
+    p_tile += warp;
+    settle();
+  }
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0]);
+  auto issue = [&]() {
+    if (p_left > 0) {
+      const bool ok = (unsigned)p_block < (unsigned)a.c.num_blocks;
+      if (lane == 0) sm.page_ok[warp][p_stage] = ok;
+      if (ok) {
+        const int off = (p_tile * kTok) & ((1 << log_bs) - 1);
+        const uint8_t* page = a.c.pool + ((size_t)p_block * Hkv + p_g) * page_bytes;
+        const uint8_t* kc = page + Q4Page<D>::code(0, log_bs, off);
+        const uint8_t* vc = page + Q4Page<D>::code(1, log_bs, off);
+        const uint32_t dst = ring + p_stage * S::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const int id = lane + 32 * i, t = id / (D / 32), ch = id % (D / 32);
+          // K rows so that a quarter (half) warp's reads cover all banks
+          const int kr = D == 128 ? t : ((t & 9) | ((t & 4) >> 1) | ((t & 2) << 1));
+          const int vr = 4 * (t & 3) + (t >> 2);
+          const int vch = D == 128 ? ch ^ (2 * ((t >> 3) & 1)) : ch;
+          cp_async16(dst + kr * (D / 2) + ch * 16, kc + id * 16);
+          cp_async16(dst + S::kCodes + vr * (D / 2) + vch * 16, vc + id * 16);
+        }
+        if (lane < D / 8) {
+          const int which = lane >= D / 16, ch = lane % (D / 16);
+          cp_async16(dst + 2 * S::kCodes + which * S::kScales + ch * 16,
+                     page + Q4Page<D>::scale(which, log_bs, off) + ch * 16);
+        }
+      } else if (a.status && lane == 0) {
+        atomicOr(a.status, WAITS_DEV_BAD_INDEX);
+      }
+      p_stage = p_stage + 1 == kStages ? 0 : p_stage + 1;
+      if (--p_left > 0) {
+        p_tile += kWarps;
+        settle();
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue();
+
+  // ---- the run, item by item
+  int stage = 0;
+  bool first = true;
+  if (tid == 0) a.desc[blockIdx.x].parts = 0;
+  for (int64_t u = u0; u < u1;) {
+    const int n = tokens(s);
+    const int64_t piece = u1 - u < nt - tile0 ? u1 - u : nt - tile0;
+    // Q fragments: head r (and r + 8), dimensions 16 k + 4 c .. + 3
+    uint32_t qf[NT][D / 16][2];
+    float qscale[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int h = r + 8 * t;
+      uint2 raw[D / 16];
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        raw[k] = make_uint2(0, 0);
+        if (h < G)
+          raw[k] = __ldg(reinterpret_cast<const uint2*>(
+              a.q + ((size_t)s * a.Hq + (size_t)g * G + h) * D + 16 * k + 4 * c));
+        top = max(top, max(max(raw[k].x & 0x7fffu, (raw[k].x >> 16) & 0x7fffu),
+                           max(raw[k].y & 0x7fffu, (raw[k].y >> 16) & 0x7fffu)));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = (int)(top >> 7) - 127 - 13;              // the largest in [2^13, 2^14)
+      e = e < -126 ? -126 : e;
+      const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
+      qscale[t] = a.scale_log2 * exp2f((float)e);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[t][k][0] = pack_half(bf16_lo(raw[k].x) * mul, bf16_hi(raw[k].x) * mul);
+        qf[t][k][1] = pack_half(bf16_lo(raw[k].y) * mul, bf16_hi(raw[k].y) * mul);
+      }
+    }
+    float o[NT][NG][2][4], m[NT], l[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = -INFINITY;
+      l[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG * 8; ++i) o[t][i / 8][i / 4 % 2][i % 4] = 0.f;
+    }
+    // V's unit per group: scale * unit < 2^kScaleRoom while scale <= limit
+    uint32_t unit[NW2], limit[NW2];
+#pragma unroll
+    for (int i = 0; i < NW2; ++i) {
+      unit[i] = 0x7e807e80u;                           // 2^126
+      limit[i] = 0x03800380u;                          // 2^-120
+    }
+    int64_t k0 = u - u0;                               // first tile of this warp in the piece
+    k0 += (warp - k0 % kWarps + kWarps) % kWarps;
+    for (int64_t k = k0; k < u - u0 + piece; k += kWarps) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      issue();
+      const uint8_t* st = &sm.ring[warp][stage][0];
+      const bool ok = sm.page_ok[warp][stage];
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      const int valid = ok ? n - (tile0 + (int)(k - (u - u0))) * kTok : 0;
+      // scales of tokens 4 c .. 4 c + 3, groups two to a word
+      uint32_t ks[4][NW2], vs[4][NW2];
+#pragma unroll
+      for (int i = 0; i < NW2; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + 2 * S::kCodes + 16 * (NW2 * c + i));
+        const uint4 y =
+            *reinterpret_cast<const uint4*>(st + 2 * S::kCodes + S::kScales + 16 * (NW2 * c + i));
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ks[(4 * i + j) / NW2][(4 * i + j) % NW2] = xs[j];
+          vs[(4 * i + j) / NW2][(4 * i + j) % NW2] = ys[j];
+        }
+      }
+      // logits: S[head, token] per group, scaled by K's scales
+      float lg[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) lg[t][0] = lg[t][1] = lg[t][2] = lg[t][3] = 0.f;
+#pragma unroll
+      for (int jt = 0; jt < 2; ++jt) {
+        const int p = 4 * (r >> 1) + (r & 1) + 2 * jt;
+        uint32_t kw[NG];
+        if (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + p * 64 + 16 * c);
+          kw[0] = x.x;
+          kw[1] = x.y;
+          kw[NG - 2] = x.z;
+          kw[NG - 1] = x.w;
+        } else {
+          const int kr = (p & 9) | ((p & 4) >> 1) | ((p & 2) << 1);
+          const uint2 x = *reinterpret_cast<const uint2*>(st + kr * 32 + 8 * c);
+          kw[0] = x.x;
+          kw[1] = x.y;
+        }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          uint32_t h[4];
+          e2m1_to_half(kw[gr], h);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(acc, qf[0][2 * gr][0], NT > 1 ? qf[NT - 1][2 * gr][0] : 0u, qf[0][2 * gr][1],
+                   NT > 1 ? qf[NT - 1][2 * gr][1] : 0u, h[0], h[1]);
+          mma16816(acc, qf[0][2 * gr + 1][0], NT > 1 ? qf[NT - 1][2 * gr + 1][0] : 0u,
+                   qf[0][2 * gr + 1][1], NT > 1 ? qf[NT - 1][2 * gr + 1][1] : 0u, h[2], h[3]);
+          const uint32_t s0 = ks[2 * jt][gr / 2], s1 = ks[2 * jt + 1][gr / 2];
+          const float f0 = gr % 2 ? bf16_hi(s0) : bf16_lo(s0);
+          const float f1 = gr % 2 ? bf16_hi(s1) : bf16_lo(s1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            lg[t][2 * jt] = fmaf(acc[2 * t], f0, lg[t][2 * jt]);
+            lg[t][2 * jt + 1] = fmaf(acc[2 * t + 1], f1, lg[t][2 * jt + 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lg[t][j] *= qscale[t];
+      if (valid < kTok) {                              // the slots past the end hold anything
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * c + j >= valid) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) lg[t][j] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NW2; ++i) vs[j][i] = 0;
+          }
+      }
+      // the running maximum moves, and the sums with it, when it lags by 2^kSlack
+      bool move = false;
+      float top[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        top[t] = fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3]));
+        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 1));
+        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 2));
+        move |= top[t] > m[t] + kSlack;
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float to = top[t] > m[t] + kSlack ? top[t] : m[t];
+          const float f = to == -INFINITY ? 1.f : exp2f(m[t] - to);
+          m[t] = to;
+          l[t] *= f;
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * c);
+          const float f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+#pragma unroll
+          for (int i = 0; i < NG * 2; ++i) {
+            o[t][i / 2][i % 2][0] *= f0;
+            o[t][i / 2][i % 2][1] *= f1;
+            o[t][i / 2][i % 2][2] *= f0;
+            o[t][i / 2][i % 2][3] *= f1;
+          }
+        }
+      }
+      // V's scales outgrow their unit (a NaN never fits and passes through)
+      bool grow = false;
+#pragma unroll
+      for (int i = 0; i < NW2; ++i) {
+        const uint32_t x = __vimax3_u16x2(__vimax3_u16x2(vs[0][i], vs[1][i], vs[2][i]), vs[3][i],
+                                          limit[i]);
+        grow |= x != limit[i];
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          uint32_t x = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t b = (gr % 2 ? vs[j][gr / 2] >> 16 : vs[j][gr / 2]) & 0xffffu;
+            x = b < 0x7f80u ? max(x, b) : x;
+          }
+          x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const int sh = 16 * (gr % 2);
+          const uint32_t mask = 0xffffu << sh;
+          const uint32_t was = (unit[gr / 2] >> sh) & 0xffffu;
+          if (x > ((limit[gr / 2] >> sh) & 0xffffu)) {
+            int e = (int)(x >> 7) - 127;               // the largest scale in [1, 2)
+            e = e > 126 ? 126 : e;
+            const uint32_t to = (uint32_t)(127 - e) << 7;
+            const uint32_t lim = (uint32_t)min(127 + e + kScaleRoom, 254) << 7;
+            unit[gr / 2] = (unit[gr / 2] & ~mask) | (to << sh);
+            limit[gr / 2] = (limit[gr / 2] & ~mask) | (lim << sh);
+            const float f = exp2f((float)((int)(to >> 7) - (int)(was >> 7)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[t][gr][i / 4][i % 4] *= f;
+          }
+        }
+      }
+      float p[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float ref = m[t] == -INFINITY ? 0.f : m[t];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[t][j] = ex2(lg[t][j] - ref);
+          l[t] += p[t][j];
+        }
+      }
+      // O^T[d, head] += V^T[d, token] (p scale)[token, head], group by group
+      uint32_t vw[4][NW2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (D == 128) {
+          const uint2 x = *reinterpret_cast<const uint2*>(
+              st + S::kCodes + (4 * j + c) * 64 + (((r >> 1) ^ (2 * (c >> 1))) * 16) + 8 * (r & 1));
+          vw[j][0] = x.x;
+          vw[j][NW2 - 1] = x.y;
+        } else {
+          vw[j][0] = *reinterpret_cast<const uint32_t*>(st + S::kCodes + (4 * j + c) * 32 + 4 * r);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NW2; ++i) {
+        // tokens j, j + 1 of one dimension into one byte; even, odd dimensions
+        uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+          const uint32_t w0 = vw[2 * jp][i], w1 = vw[2 * jp + 1][i];
+          e2m1_to_half((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), lo[jp]);
+          e2m1_to_half(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), hi[jp]);
+        }
+        uint32_t sc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[j] = mul_bf16x2(vs[j][i], unit[i]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int gr = 2 * i + half;
+          float f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = half ? bf16_hi(sc[j]) : bf16_lo(sc[j]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint32_t b0 = pack_half(p[t][0] * f[0], p[t][1] * f[1]);
+            const uint32_t b1 = pack_half(p[t][2] * f[2], p[t][3] * f[3]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+              mma16816(o[t][gr][mt], lo[0][2 * half + mt], hi[0][2 * half + mt],
+                       lo[1][2 * half + mt], hi[1][2 * half + mt], b0, b1);
+          }
+        }
+      }
+    }
+    // ---- the item's end: join the warps' sums
+    const bool whole = piece == nt;
+    float* part = a.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * part_floats(G, D);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float x = l[t];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if (c == 0) {
+        sm.m[warp][r + 8 * t] = m[t];
+        sm.l[warp][r + 8 * t] = x;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int h = 2 * c + b;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][h + 8 * t]);
+        const float mw = sm.m[warp][h + 8 * t];
+        const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const uint32_t un = (unit[gr / 2] >> (16 * (gr % 2) + 7)) & 0xffu;
+          const float v = exp2f((float)(127 - (int)un));
+          *reinterpret_cast<float4*>(&sm.o[warp][h][32 * gr + 4 * r]) =
+              make_float4(o[t][gr][0][b] * v * f, o[t][gr][0][2 + b] * v * f,
+                          o[t][gr][1][b] * v * f, o[t][gr][1][2 + b] * v * f);
+        }
+      }
+      __syncthreads();
+      const int heads = G - 8 * t < 8 ? G - 8 * t : 8;
+      for (int i = tid; i < heads * (D / 4); i += kThreads) {
+        const int h = i / (D / 4), d4 = 4 * (i % (D / 4));
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][h + 8 * t]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = sm.m[w][h + 8 * t];
+          L += sm.l[w][h + 8 * t] * (mw == -INFINITY ? 0.f : exp2f(mw - M));
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][h][d4]);
+          acc.x += x.x;
+          acc.y += x.y;
+          acc.z += x.z;
+          acc.w += x.w;
+        }
+        const int hh = h + 8 * t;
+        if (whole) {
+          const size_t row = (size_t)s * a.Hq + (size_t)g * G + hh;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<uint2*>(a.out + row * D + d4) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+          if (a.lse && d4 == 0)
+            a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(part + (size_t)hh * D + d4) = acc;
+          if (d4 == 0) {
+            part[(size_t)G * D + hh] = M;
+            part[(size_t)G * D + G + hh] = L;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // the first part of an item that goes on in the next CTAs
+    if (!whole && tile0 == 0 && tid == 0) {
+      const int64_t end = u + nt;                      // where the item ends; its last CTA
+      const int64_t last = (end * ctas - 1) / total;
+      a.desc[blockIdx.x] = Desc{s, g, (int32_t)(last - blockIdx.x + 1), first ? 0 : 1};
+    }
+    u += piece;
+    tile0 = 0;
+    first = false;
+    if (u < u1 && ++g == Hkv) {
+      g = 0;
+      do ++s; while ((nt = tiles(s)) == 0);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the parts of an item: grid (CTAs of the first kernel, G), D threads.
+template <int D>
+__global__ void __launch_bounds__(D) q4_join_kernel(const DecodeArgs a) {
+  pdl_allow_next();
+  pdl_wait();
+  const Desc de = a.desc[blockIdx.x];
+  if (de.parts == 0) return;
+  const int h = blockIdx.y, t = threadIdx.x, G = a.G;
+  const size_t stride = part_floats(G, D);
+  // part 0 in this CTA's slot, the others in the first slots of the next CTAs
+  auto at = [&](int i) {
+    return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? de.slot : 0)) * stride;
+  };
+  float M = -INFINITY;
+  for (int i = 0; i < de.parts; ++i) M = fmaxf(M, at(i)[(size_t)G * D + h]);
+  float L = 0.f, acc = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < de.parts; ++i) {
+    const float* p = at(i);
+    const float m = p[(size_t)G * D + h];
+    const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+    L = fmaf(p[(size_t)G * D + G + h], f, L);
+    acc = fmaf(p[(size_t)h * D + t], f, acc);
+  }
+  const size_t row = (size_t)de.s * a.Hq + (size_t)de.g * G + h;
+  const float v = L == 0.f ? 0.f : acc / L;
+  a.out[row * D + t] = (uint16_t)(pack_bf16(v, 0.f) & 0xffffu);
+  if (a.lse && t == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The CTAs that the workspace has room for: every SM of a B200, twice.
+constexpr int kMaxCtas = 148 * kCtasPerSm;
+
+template <int D, int NT>
+cudaError_t launch_d(const DecodeArgs& a, int ctas, cudaStream_t st) {
+  const size_t smem = sizeof(Smem<D>);
+  cudaError_t err = cudaFuncSetAttribute(q4_decode_kernel<D, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(q4_decode_kernel<D, NT>, dim3(ctas), dim3(kThreads), smem, st, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(q4_join_kernel<D>, dim3(ctas, a.G), dim3(D), 0, st, a);
 }
 
 }  // namespace
 
-size_t q4_decode_workspace_bytes(const Q4Pool&, int, int) { return 16; }
+size_t q4_decode_workspace_bytes(const Q4Pool& c, int, int Hq) {
+  return kMaxCtas * (sizeof(Desc) + 2 * part_floats(Hq / c.Hkv, c.d) * sizeof(float));
+}
 
 cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const uint16_t* q,
                              const int32_t* table, const int32_t* len, uint16_t* out, float* lse,
-                             void*, uint32_t* status, cudaStream_t st) {
-  const float scale = (float)(1.4426950408889634 / std::sqrt((double)c.d));
-  auto kernel = c.d == 64 ? q4_decode_kernel<64> : q4_decode_kernel<128>;
-  return launch_pdl(kernel, dim3(c.Hkv, nseq), dim3(kWarps * 32), 0, st, c, Hq, width, q, table,
-                    len, out, lse, scale, status);
+                             void* ws, uint32_t* status, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess)
+    err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err != cudaSuccess) return err;
+  const int ctas = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
+  Desc* desc = static_cast<Desc*>(ws);
+  const DecodeArgs a{c, nseq, Hq, Hq / c.Hkv, width, q, table, len, out, lse,
+                     reinterpret_cast<float*>(desc + kMaxCtas), desc, status,
+                     (float)(1.4426950408889634 / std::sqrt((double)c.d))};
+  const bool wide = a.G > 8;
+  if (c.d == 64) return wide ? launch_d<64, 2>(a, ctas, st) : launch_d<64, 1>(a, ctas, st);
+  return wide ? launch_d<128, 2>(a, ctas, st) : launch_d<128, 1>(a, ctas, st);
 }
 
 }  // namespace waits
