@@ -617,12 +617,10 @@ __global__ void __launch_bounds__(D) q4_join_kernel(const DecodeArgs a) {
 constexpr int kMaxCtas = 148 * kCtasPerSm;
 
 template <int D, int NT>
-cudaError_t launch_d(const DecodeArgs& a, int ctas, cudaStream_t st) {
-  const size_t smem = sizeof(Smem<D>);
-  cudaError_t err = cudaFuncSetAttribute(q4_decode_kernel<D, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err != cudaSuccess) return err;
-  err = launch_pdl(q4_decode_kernel<D, NT>, dim3(ctas), dim3(kThreads), smem, st, a);
+cudaError_t launch_d(const DecodeArgs& a, int dev, int ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, NT>, dim3(ctas),
+                                          dim3(kThreads), sizeof(Smem<D>), st, a);
   if (err != cudaSuccess) return err;
   return launch_pdl(q4_join_kernel<D>, dim3(ctas, a.G), dim3(D), 0, st, a);
 }
@@ -637,9 +635,7 @@ cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const
                              const int32_t* table, const int32_t* len, uint16_t* out, float* lse,
                              void* ws, uint32_t* status, cudaStream_t st) {
   int dev = 0, sms = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err == cudaSuccess)
-    err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const cudaError_t err = current_sms(&dev, &sms);
   if (err != cudaSuccess) return err;
   const int ctas = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
   Desc* desc = static_cast<Desc*>(ws);
@@ -647,8 +643,8 @@ cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const
                      reinterpret_cast<float*>(desc + kMaxCtas), desc, status,
                      (float)(1.4426950408889634 / std::sqrt((double)c.d))};
   const bool wide = a.G > 8;
-  if (c.d == 64) return wide ? launch_d<64, 2>(a, ctas, st) : launch_d<64, 1>(a, ctas, st);
-  return wide ? launch_d<128, 2>(a, ctas, st) : launch_d<128, 1>(a, ctas, st);
+  if (c.d == 64) return wide ? launch_d<64, 2>(a, dev, ctas, st) : launch_d<64, 1>(a, dev, ctas, st);
+  return wide ? launch_d<128, 2>(a, dev, ctas, st) : launch_d<128, 1>(a, dev, ctas, st);
 }
 
 }  // namespace waits

@@ -3,6 +3,7 @@
 // forgetting-curve weight, and small block-level helpers.
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -307,6 +308,39 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The current device and its SMs, the count looked up once per device.
+inline cudaError_t current_sms(int* dev, int* sms) {
+  static std::atomic<int> known[64];
+  cudaError_t err = cudaGetDevice(dev);
+  if (err != cudaSuccess) return err;
+  if (*dev < 64 && (*sms = known[*dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+  if (err == cudaSuccess && *dev < 64) known[*dev].store(*sms, std::memory_order_relaxed);
+  return err;
+}
+
+// launch_pdl for a kernel that needs more than 48 KB of dynamic shared
+// memory.  The opt-in is made once per device (`done`: a bit each); should
+// the launch be refused, because a new context has forgotten it, it is made
+// again.  The opt-in costs about a third of a launch on the host.
+template <typename Kernel, typename... Args>
+cudaError_t launch_pdl_smem(std::atomic<uint64_t>& done, int dev, Kernel kernel, dim3 grid,
+                            dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  const bool fresh = !(done.load(std::memory_order_relaxed) & bit);
+  for (int tries = fresh ? 1 : 2;; --tries) {
+    if (fresh || tries == 1) {
+      const cudaError_t err =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
+      done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const cudaError_t err = launch_pdl(kernel, grid, block, smem, stream, args...);
+    if (err != cudaErrorInvalidValue || tries == 1) return err;
+    cudaGetLastError();
+  }
 }
 
 // Extra text appended to the next waits_last_error() message (host only).
