@@ -4,7 +4,7 @@
 // scale.  HBM bounds it: 1.125 d bytes per (token, KV head), read once for
 // all G query heads of the group.
 //
-// Split: the work is the list of all 16-token tiles of all (sequence, KV
+// Split: the work is the list of all 32-token tiles of all (sequence, KV
 // head) items, and every CTA takes an equal run of it, whatever the lengths
 // (they are known on the device only).  A run covers whole items, whose
 // output it writes, and at most two parts of items, whose (weighted sum,
@@ -33,8 +33,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTok = 16;              // tokens per tile
-constexpr int kStages = 4;
+constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
+constexpr int kTok = 2 * kSub;        // tokens per tile
+constexpr int kStages = 2;
 constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
@@ -61,6 +62,35 @@ __device__ inline void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with C = 0.
+__device__ inline void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                     uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Two fp32 values in one register pair.
+__device__ inline uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ inline float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ inline uint32_t pack_half(float lo, float hi) {
   uint32_t r;
@@ -93,14 +123,15 @@ __device__ inline int64_t warp_sum(int64_t x) {
 
 template <int D>
 struct Smem {
-  static constexpr int kTileBytes = kTok * D * 9 / 8;
-  static constexpr int kCodes = kTok * D / 2;           // bytes of one tile's K (or V) codes
-  static constexpr int kScales = kTok * D / 16;
+  static constexpr int kCodes = kSub * D / 2;           // bytes of a half tile's K (or V) codes
+  static constexpr int kScales = kSub * D / 16;
+  static constexpr int kHalf = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+  static constexpr int kTileBytes = 2 * kHalf;
   static constexpr int kRow = D + 4;                    // floats per merge row, no bank conflicts
   uint8_t ring[kWarps][kStages][kTileBytes];
   float o[kWarps][8][kRow];
   float m[kWarps][16], l[kWarps][16];
-  int32_t page_ok[kWarps][kStages];
+  int32_t page_ok[kWarps][kStages][2];
   int64_t scan[kWarps];
   int64_t total;
   int64_t where[2];                                     // sequence of the run's start, units before it
@@ -192,11 +223,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
   const int64_t in_seq = u0 - sm.where[1];
   int g = (int)(in_seq / nt), tile0 = (int)(in_seq - (int64_t)g * nt);
 
-  // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..
-  int64_t p_left = (u1 - u0 - warp + kWarps - 1) / kWarps;   // tiles not yet issued
-  if (u1 - u0 <= warp) p_left = 0;
+  // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..  A half warp
+  // copies a half tile, whose page it looks up one tile ahead.
+  int p_left = 0;                          // tiles not yet issued
+  if (u1 - u0 > warp) p_left = (int)((u1 - u0 - warp + kWarps - 1) / kWarps);
   int p_s = s, p_g = g, p_nt = nt, p_tile = tile0, p_stage = 0, p_block = -1;
-  auto settle = [&]() {      // bring p_tile into its item; load its block
+  const int half = lane >> 4, hl = lane & 15;
+  auto settle = [&]() {                    // bring p_tile into its item; load the half's block
     while (p_tile >= p_nt) {
       p_tile -= p_nt;
       if (++p_g == Hkv) {
@@ -204,42 +237,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
         do ++p_s; while ((p_nt = tiles(p_s)) == 0);
       }
     }
-    p_block = __ldg(a.table + (int64_t)p_s * a.width + (((int64_t)p_tile * kTok) >> log_bs));
+    const int j = p_tile * kTok + half * kSub;   // a tile's second half may lie past the end
+    p_block = j < tokens(p_s) ? __ldg(a.table + (int64_t)p_s * a.width + (j >> log_bs)) : -2;
   };
   if (p_left > 0) {
     p_tile += warp;
     settle();
   }
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0]);
+  // where a lane's 16-byte pieces of a half go: K rows and V rows in orders
+  // that keep the fragment reads free of bank conflicts
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0]) + half * S::kHalf;
+  auto k_dst = [&](int id) -> uint32_t {
+    const int t = id / NG, ch = id % NG;
+    const int kr = D == 128 ? t : ((t & 9) | ((t & 4) >> 1) | ((t & 2) << 1));
+    return kr * (D / 2) + ch * 16;
+  };
+  auto v_dst = [&](int id) -> uint32_t {
+    const int t = id / NG, ch = id % NG;
+    const int vr = 4 * (t & 3) + (t >> 2);
+    return S::kCodes + vr * (D / 2) + (D == 128 ? ch ^ (2 * ((t >> 3) & 1)) : ch) * 16;
+  };
   auto issue = [&]() {
     if (p_left > 0) {
       const bool ok = (unsigned)p_block < (unsigned)a.c.num_blocks;
-      if (lane == 0) sm.page_ok[warp][p_stage] = ok;
+      if (hl == 0) sm.page_ok[warp][p_stage][half] = ok;
       if (ok) {
-        const int off = (p_tile * kTok) & ((1 << log_bs) - 1);
+        const int off = (p_tile * kTok + half * kSub) & ((1 << log_bs) - 1);
         const uint8_t* page = a.c.pool + ((size_t)p_block * Hkv + p_g) * page_bytes;
-        const uint8_t* kc = page + Q4Page<D>::code(0, log_bs, off);
-        const uint8_t* vc = page + Q4Page<D>::code(1, log_bs, off);
+        const uint8_t* kc = page + Q4Page<D>::code(0, log_bs, off) + hl * 16;
+        const uint8_t* vc = page + Q4Page<D>::code(1, log_bs, off) + hl * 16;
         const uint32_t dst = ring + p_stage * S::kTileBytes;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const int id = lane + 32 * i, t = id / (D / 32), ch = id % (D / 32);
-          // K rows so that a quarter (half) warp's reads cover all banks
-          const int kr = D == 128 ? t : ((t & 9) | ((t & 4) >> 1) | ((t & 2) << 1));
-          const int vr = 4 * (t & 3) + (t >> 2);
-          const int vch = D == 128 ? ch ^ (2 * ((t >> 3) & 1)) : ch;
-          cp_async16(dst + kr * (D / 2) + ch * 16, kc + id * 16);
-          cp_async16(dst + S::kCodes + vr * (D / 2) + vch * 16, vc + id * 16);
+        for (int i = 0; i < D / 32; ++i) {
+          cp_async16(dst + k_dst(hl + 16 * i), kc + i * 256);
+          cp_async16(dst + v_dst(hl + 16 * i), vc + i * 256);
         }
-        if (lane < D / 8) {
-          const int which = lane >= D / 16, ch = lane % (D / 16);
+        if (D == 128 || hl < D / 8) {
+          const int which = hl >= D / 16, ch = hl % (D / 16);
           cp_async16(dst + 2 * S::kCodes + which * S::kScales + ch * 16,
                      page + Q4Page<D>::scale(which, log_bs, off) + ch * 16);
         }
-      } else if (a.status && lane == 0) {
+      } else if (a.status && p_block != -2 && hl == 0) {
         atomicOr(a.status, WAITS_DEV_BAD_INDEX);
       }
-      p_stage = p_stage + 1 == kStages ? 0 : p_stage + 1;
+      p_stage ^= 1;
       if (--p_left > 0) {
         p_tile += kWarps;
         settle();
@@ -247,8 +288,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue();
+  issue();
 
   // ---- the run, item by item
   int stage = 0;
@@ -301,81 +341,83 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       unit[i] = 0x7e807e80u;                           // 2^126
       limit[i] = 0x03800380u;                          // 2^-120
     }
-    int64_t k0 = u - u0;                               // first tile of this warp in the piece
-    k0 += (warp - k0 % kWarps + kWarps) % kWarps;
-    for (int64_t k = k0; k < u - u0 + piece; k += kWarps) {
-      cp_async_wait<kStages - 2>();
+    int k0 = (int)(u - u0);                            // first tile of this warp in the piece
+    const int kend = k0 + (int)piece, base = k0 - tile0;
+    k0 += (warp - k0) & (kWarps - 1);
+    for (int k = k0; k < kend; k += kWarps) {
+      cp_async_wait<0>();
       __syncwarp();
       issue();
       const uint8_t* st = &sm.ring[warp][stage][0];
-      const bool ok = sm.page_ok[warp][stage];
-      stage = stage + 1 == kStages ? 0 : stage + 1;
-      const int valid = ok ? n - (tile0 + (int)(k - (u - u0))) * kTok : 0;
-      // scales of tokens 4 c .. 4 c + 3, groups two to a word
-      uint32_t ks[4][NW2], vs[4][NW2];
+      const int valid = n - (k - base) * kTok;
+      const int2 ok = *reinterpret_cast<const int2*>(&sm.page_ok[warp][stage][0]);
+      stage ^= 1;
+      const bool edge = valid < kTok || !ok.x || !ok.y;
+      // logits: S[head, token] per group, scaled by K's scales; lane: head r,
+      // tokens 4 c .. 4 c + 3 of each half
+      uint64_t lg2[NT][2][2];
 #pragma unroll
-      for (int i = 0; i < NW2; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(st + 2 * S::kCodes + 16 * (NW2 * c + i));
-        const uint4 y =
-            *reinterpret_cast<const uint4*>(st + 2 * S::kCodes + S::kScales + 16 * (NW2 * c + i));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint8_t* sh = st + hf * S::kHalf;
+        uint32_t ks[4][NW2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ks[(4 * i + j) / NW2][(4 * i + j) % NW2] = xs[j];
-          vs[(4 * i + j) / NW2][(4 * i + j) % NW2] = ys[j];
-        }
-      }
-      // logits: S[head, token] per group, scaled by K's scales
-      float lg[NT][4];
+        for (int i = 0; i < NW2; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sh + 2 * S::kCodes + 16 * (NW2 * c + i));
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) lg[t][0] = lg[t][1] = lg[t][2] = lg[t][3] = 0.f;
-#pragma unroll
-      for (int jt = 0; jt < 2; ++jt) {
-        const int p = 4 * (r >> 1) + (r & 1) + 2 * jt;
-        uint32_t kw[NG];
-        if (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(st + p * 64 + 16 * c);
-          kw[0] = x.x;
-          kw[1] = x.y;
-          kw[NG - 2] = x.z;
-          kw[NG - 1] = x.w;
-        } else {
-          const int kr = (p & 9) | ((p & 4) >> 1) | ((p & 2) << 1);
-          const uint2 x = *reinterpret_cast<const uint2*>(st + kr * 32 + 8 * c);
-          kw[0] = x.x;
-          kw[1] = x.y;
+          for (int j = 0; j < 4; ++j) ks[(4 * i + j) / NW2][(4 * i + j) % NW2] = xs[j];
         }
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          uint32_t h[4];
-          e2m1_to_half(kw[gr], h);
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(acc, qf[0][2 * gr][0], NT > 1 ? qf[NT - 1][2 * gr][0] : 0u, qf[0][2 * gr][1],
-                   NT > 1 ? qf[NT - 1][2 * gr][1] : 0u, h[0], h[1]);
-          mma16816(acc, qf[0][2 * gr + 1][0], NT > 1 ? qf[NT - 1][2 * gr + 1][0] : 0u,
-                   qf[0][2 * gr + 1][1], NT > 1 ? qf[NT - 1][2 * gr + 1][1] : 0u, h[2], h[3]);
-          const uint32_t s0 = ks[2 * jt][gr / 2], s1 = ks[2 * jt + 1][gr / 2];
-          const float f0 = gr % 2 ? bf16_hi(s0) : bf16_lo(s0);
-          const float f1 = gr % 2 ? bf16_hi(s1) : bf16_lo(s1);
+        for (int jt = 0; jt < 2; ++jt) {
+          const int p = 4 * (r >> 1) + (r & 1) + 2 * jt;
+          uint32_t kw[NG];
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sh + p * 64 + 16 * c);
+            kw[0] = x.x;
+            kw[1] = x.y;
+            kw[NG - 2] = x.z;
+            kw[NG - 1] = x.w;
+          } else {
+            const int kr = (p & 9) | ((p & 4) >> 1) | ((p & 2) << 1);
+            const uint2 x = *reinterpret_cast<const uint2*>(sh + kr * 32 + 8 * c);
+            kw[0] = x.x;
+            kw[1] = x.y;
+          }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            lg[t][2 * jt] = fmaf(acc[2 * t], f0, lg[t][2 * jt]);
-            lg[t][2 * jt + 1] = fmaf(acc[2 * t + 1], f1, lg[t][2 * jt + 1]);
+          for (int gr = 0; gr < NG; ++gr) {
+            uint32_t h[4];
+            e2m1_to_half(kw[gr], h);
+            float acc[4];
+            mma16816_zero(acc, qf[0][2 * gr][0], NT > 1 ? qf[NT - 1][2 * gr][0] : 0u,
+                          qf[0][2 * gr][1], NT > 1 ? qf[NT - 1][2 * gr][1] : 0u, h[0], h[1]);
+            mma16816(acc, qf[0][2 * gr + 1][0], NT > 1 ? qf[NT - 1][2 * gr + 1][0] : 0u,
+                     qf[0][2 * gr + 1][1], NT > 1 ? qf[NT - 1][2 * gr + 1][1] : 0u, h[2], h[3]);
+            const uint32_t s0 = ks[2 * jt][gr / 2], s1 = ks[2 * jt + 1][gr / 2];
+            const uint64_t f =
+                gr % 2 ? pair(bf16_hi(s0), bf16_hi(s1)) : pair(bf16_lo(s0), bf16_lo(s1));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint64_t x = pair(acc[2 * t], acc[2 * t + 1]);
+              lg2[t][hf][jt] = gr == 0 ? mul2(x, f) : fma2(x, f, lg2[t][hf][jt]);
+            }
           }
         }
       }
+      float lg[NT][8];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) lg[t][j] *= qscale[t];
-      if (valid < kTok) {                              // the slots past the end hold anything
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpair(lg2[t][i / 2][i % 2]);
+          lg[t][2 * i] = x.x * qscale[t];
+          lg[t][2 * i + 1] = x.y * qscale[t];
+        }
+      if (edge) {                                      // the slots past the end hold anything
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * c + j >= valid) {
+        for (int i = 0; i < 8; ++i)
+          if (16 * (i / 4) + 4 * c + i % 4 >= valid || !(i < 4 ? ok.x : ok.y)) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) lg[t][j] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NW2; ++i) vs[j][i] = 0;
+            for (int t = 0; t < NT; ++t) lg[t][i] = -INFINITY;
           }
       }
       // the running maximum moves, and the sums with it, when it lags by 2^kSlack
@@ -383,14 +425,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       float top[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        top[t] = fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3]));
-        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 1));
-        top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 2));
+        top[t] = fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
+                       fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7])));
         move |= top[t] > m[t] + kSlack;
       }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+          top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 1));
+          top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 2));
           const float to = top[t] > m[t] + kSlack ? top[t] : m[t];
           const float f = to == -INFINITY ? 1.f : exp2f(m[t] - to);
           m[t] = to;
@@ -406,93 +449,116 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
           }
         }
       }
-      // V's scales outgrow their unit (a NaN never fits and passes through)
-      bool grow = false;
-#pragma unroll
-      for (int i = 0; i < NW2; ++i) {
-        const uint32_t x = __vimax3_u16x2(__vimax3_u16x2(vs[0][i], vs[1][i], vs[2][i]), vs[3][i],
-                                          limit[i]);
-        grow |= x != limit[i];
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          uint32_t x = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t b = (gr % 2 ? vs[j][gr / 2] >> 16 : vs[j][gr / 2]) & 0xffffu;
-            x = b < 0x7f80u ? max(x, b) : x;
-          }
-          x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const int sh = 16 * (gr % 2);
-          const uint32_t mask = 0xffffu << sh;
-          const uint32_t was = (unit[gr / 2] >> sh) & 0xffffu;
-          if (x > ((limit[gr / 2] >> sh) & 0xffffu)) {
-            int e = (int)(x >> 7) - 127;               // the largest scale in [1, 2)
-            e = e > 126 ? 126 : e;
-            const uint32_t to = (uint32_t)(127 - e) << 7;
-            const uint32_t lim = (uint32_t)min(127 + e + kScaleRoom, 254) << 7;
-            unit[gr / 2] = (unit[gr / 2] & ~mask) | (to << sh);
-            limit[gr / 2] = (limit[gr / 2] & ~mask) | (lim << sh);
-            const float f = exp2f((float)((int)(to >> 7) - (int)(was >> 7)));
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[t][gr][i / 4][i % 4] *= f;
-          }
-        }
-      }
-      float p[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float ref = m[t] == -INFINITY ? 0.f : m[t];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p[t][j] = ex2(lg[t][j] - ref);
-          l[t] += p[t][j];
+        for (int i = 0; i < 8; ++i) {
+          lg[t][i] = ex2(lg[t][i] - ref);
+          l[t] += lg[t][i];
         }
       }
       // O^T[d, head] += V^T[d, token] (p scale)[token, head], group by group
-      uint32_t vw[4][NW2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (D == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(
-              st + S::kCodes + (4 * j + c) * 64 + (((r >> 1) ^ (2 * (c >> 1))) * 16) + 8 * (r & 1));
-          vw[j][0] = x.x;
-          vw[j][NW2 - 1] = x.y;
-        } else {
-          vw[j][0] = *reinterpret_cast<const uint32_t*>(st + S::kCodes + (4 * j + c) * 32 + 4 * r);
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint8_t* sh = st + hf * S::kHalf;
+        uint32_t vs[4][NW2];
+#pragma unroll
+        for (int i = 0; i < NW2; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sh + 2 * S::kCodes + S::kScales +
+                                                          16 * (NW2 * c + i));
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) vs[(4 * i + j) / NW2][(4 * i + j) % NW2] = xs[j];
         }
-      }
+        if (edge) {
 #pragma unroll
-      for (int i = 0; i < NW2; ++i) {
-        // tokens j, j + 1 of one dimension into one byte; even, odd dimensions
-        uint32_t lo[2][4], hi[2][4];
+          for (int j = 0; j < 4; ++j)
+            if (16 * hf + 4 * c + j >= valid || !(hf ? ok.y : ok.x)) {
 #pragma unroll
-        for (int jp = 0; jp < 2; ++jp) {
-          const uint32_t w0 = vw[2 * jp][i], w1 = vw[2 * jp + 1][i];
-          e2m1_to_half((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), lo[jp]);
-          e2m1_to_half(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), hi[jp]);
+              for (int i = 0; i < NW2; ++i) vs[j][i] = 0;
+            }
         }
-        uint32_t sc[4];
+        // V's scales outgrow their unit (a NaN never fits and passes through)
+        bool grow = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[j] = mul_bf16x2(vs[j][i], unit[i]);
+        for (int i = 0; i < NW2; ++i) {
+          const uint32_t x = __vimax3_u16x2(__vimax3_u16x2(vs[0][i], vs[1][i], vs[2][i]),
+                                            vs[3][i], limit[i]);
+          grow |= x != limit[i];
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int gr = 2 * i + half;
-          float f[4];
+          for (int gr = 0; gr < NG; ++gr) {
+            uint32_t x = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = half ? bf16_hi(sc[j]) : bf16_lo(sc[j]);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t b = (gr % 2 ? vs[j][gr / 2] >> 16 : vs[j][gr / 2]) & 0xffffu;
+              x = b < 0x7f80u ? max(x, b) : x;
+            }
+            x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            const int sft = 16 * (gr % 2);
+            const uint32_t mask = 0xffffu << sft;
+            const uint32_t was = (unit[gr / 2] >> sft) & 0xffffu;
+            if (x > ((limit[gr / 2] >> sft) & 0xffffu)) {
+              int e = (int)(x >> 7) - 127;             // the largest scale in [1, 2)
+              e = e > 126 ? 126 : e;
+              const uint32_t to = (uint32_t)(127 - e) << 7;
+              const uint32_t lim = (uint32_t)min(127 + e + kScaleRoom, 254) << 7;
+              unit[gr / 2] = (unit[gr / 2] & ~mask) | (to << sft);
+              limit[gr / 2] = (limit[gr / 2] & ~mask) | (lim << sft);
+              const float f = exp2f((float)((int)(to >> 7) - (int)(was >> 7)));
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint32_t b0 = pack_half(p[t][0] * f[0], p[t][1] * f[1]);
-            const uint32_t b1 = pack_half(p[t][2] * f[2], p[t][3] * f[3]);
+              for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-              mma16816(o[t][gr][mt], lo[0][2 * half + mt], hi[0][2 * half + mt],
-                       lo[1][2 * half + mt], hi[1][2 * half + mt], b0, b1);
+                for (int i = 0; i < 8; ++i) o[t][gr][i / 4][i % 4] *= f;
+            }
+          }
+        }
+        uint32_t vw[4][NW2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(
+                sh + S::kCodes + (4 * j + c) * 64 + (((r >> 1) ^ (2 * (c >> 1))) * 16) +
+                8 * (r & 1));
+            vw[j][0] = x.x;
+            vw[j][NW2 - 1] = x.y;
+          } else {
+            vw[j][0] = *reinterpret_cast<const uint32_t*>(sh + S::kCodes + (4 * j + c) * 32 + 4 * r);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NW2; ++i) {
+          // tokens j, j + 1 of one dimension into one byte; even, odd dimensions
+          uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+          for (int jp = 0; jp < 2; ++jp) {
+            const uint32_t w0 = vw[2 * jp][i], w1 = vw[2 * jp + 1][i];
+            e2m1_to_half((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), lo[jp]);
+            e2m1_to_half(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), hi[jp]);
+          }
+          uint32_t sc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[j] = mul_bf16x2(vs[j][i], unit[i]);
+#pragma unroll
+          for (int gh = 0; gh < 2; ++gh) {
+            const int gr = 2 * i + gh;
+            const uint64_t f01 = gh ? pair(bf16_hi(sc[0]), bf16_hi(sc[1]))
+                                    : pair(bf16_lo(sc[0]), bf16_lo(sc[1]));
+            const uint64_t f23 = gh ? pair(bf16_hi(sc[2]), bf16_hi(sc[3]))
+                                    : pair(bf16_lo(sc[2]), bf16_lo(sc[3]));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const float2 x = unpair(mul2(pair(lg[t][4 * hf], lg[t][4 * hf + 1]), f01));
+              const float2 y = unpair(mul2(pair(lg[t][4 * hf + 2], lg[t][4 * hf + 3]), f23));
+              const uint32_t b0 = pack_half(x.x, x.y), b1 = pack_half(y.x, y.y);
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+                mma16816(o[t][gr][mt], lo[0][2 * gh + mt], hi[0][2 * gh + mt], lo[1][2 * gh + mt],
+                         hi[1][2 * gh + mt], b0, b1);
+            }
           }
         }
       }
