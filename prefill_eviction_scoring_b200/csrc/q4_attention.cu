@@ -87,6 +87,11 @@ __device__ inline uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     const int n = tokens(s);
     const int64_t piece = u1 - u < nt - tile0 ? u1 - u : nt - tile0;
     // Q fragments: head r (and r + 8), dimensions 16 k + 4 c .. + 3
-    uint32_t qf[NT][D / 16][2];
+    uint32_t qf[NT][NG][4];    // per group: steps 0, 1 (first halves), steps 0, 1 (second halves)
     float qscale[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -322,15 +327,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       qscale[t] = a.scale_log2 * exp2f((float)e);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        qf[t][k][0] = pack_half(bf16_lo(raw[k].x) * mul, bf16_hi(raw[k].x) * mul);
-        qf[t][k][1] = pack_half(bf16_lo(raw[k].y) * mul, bf16_hi(raw[k].y) * mul);
+        qf[t][k / 2][k % 2] = pack_half(bf16_lo(raw[k].x) * mul, bf16_hi(raw[k].x) * mul);
+        qf[t][k / 2][2 + k % 2] = pack_half(bf16_lo(raw[k].y) * mul, bf16_hi(raw[k].y) * mul);
       }
     }
-    float o[NT][NG][2][4], m[NT], l[NT];
+    float o[NT][NG][2][4], m[NT];
+    uint64_t l2[NT];                                   // two partial sums
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       m[t] = -INFINITY;
-      l[t] = 0.f;
+      l2[t] = 0;
 #pragma unroll
       for (int i = 0; i < NG * 8; ++i) o[t][i / 8][i / 4 % 2][i % 4] = 0.f;
     }
@@ -387,18 +393,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
           for (int gr = 0; gr < NG; ++gr) {
             uint32_t h[4];
             e2m1_to_half(kw[gr], h);
-            float acc[4];
-            mma16816_zero(acc, qf[0][2 * gr][0], NT > 1 ? qf[NT - 1][2 * gr][0] : 0u,
-                          qf[0][2 * gr][1], NT > 1 ? qf[NT - 1][2 * gr][1] : 0u, h[0], h[1]);
-            mma16816(acc, qf[0][2 * gr + 1][0], NT > 1 ? qf[NT - 1][2 * gr + 1][0] : 0u,
-                     qf[0][2 * gr + 1][1], NT > 1 ? qf[NT - 1][2 * gr + 1][1] : 0u, h[2], h[3]);
             const uint32_t s0 = ks[2 * jt][gr / 2], s1 = ks[2 * jt + 1][gr / 2];
             const uint64_t f =
                 gr % 2 ? pair(bf16_hi(s0), bf16_hi(s1)) : pair(bf16_lo(s0), bf16_lo(s1));
+            float acc[4], acc2[4];
+            if (NT == 1) {
+              // rows 0 - 7 of the A quad are the heads' even step, rows 8 - 15
+              // their odd step: each product is right in one half of the rows
+              mma16816_zero(acc, qf[0][gr][0], qf[0][gr][1], qf[0][gr][2], qf[0][gr][3], h[0],
+                            h[1]);
+              mma16816_zero(acc2, qf[0][gr][0], qf[0][gr][1], qf[0][gr][2], qf[0][gr][3], h[2],
+                            h[3]);
+              uint64_t& x = lg2[0][hf][jt];
+              x = gr == 0 ? mul2(pair(acc[0], acc[1]), f) : fma2(pair(acc[0], acc[1]), f, x);
+              x = fma2(pair(acc2[2], acc2[3]), f, x);
+            } else {
+              mma16816_zero(acc, qf[0][gr][0], qf[1][gr][0], qf[0][gr][2], qf[1][gr][2], h[0],
+                            h[1]);
+              mma16816(acc, qf[0][gr][1], qf[1][gr][1], qf[0][gr][3], qf[1][gr][3], h[2], h[3]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint64_t x = pair(acc[2 * t], acc[2 * t + 1]);
-              lg2[t][hf][jt] = gr == 0 ? mul2(x, f) : fma2(x, f, lg2[t][hf][jt]);
+              for (int t = 0; t < NT; ++t) {
+                const uint64_t x = pair(acc[2 * t], acc[2 * t + 1]);
+                lg2[t][hf][jt] = gr == 0 ? mul2(x, f) : fma2(x, f, lg2[t][hf][jt]);
+              }
             }
           }
         }
@@ -409,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 x = unpair(lg2[t][i / 2][i % 2]);
-          lg[t][2 * i] = x.x * qscale[t];
-          lg[t][2 * i + 1] = x.y * qscale[t];
+          lg[t][2 * i] = x.x;
+          lg[t][2 * i + 1] = x.y;
         }
       if (edge) {                                      // the slots past the end hold anything
 #pragma unroll
@@ -426,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         top[t] = fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
-                       fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7])));
+                       fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7]))) *
+                 qscale[t];
         move |= top[t] > m[t] + kSlack;
       }
       if (__any_sync(0xffffffffu, move)) {
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
           const float to = top[t] > m[t] + kSlack ? top[t] : m[t];
           const float f = to == -INFINITY ? 1.f : exp2f(m[t] - to);
           m[t] = to;
-          l[t] *= f;
+          l2[t] = mul2(l2[t], pair(f, f));
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * c);
           const float f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
@@ -451,11 +469,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float ref = m[t] == -INFINITY ? 0.f : m[t];
+        const float ref = m[t] == -INFINITY ? 0.f : -m[t];
+        const uint64_t ref2 = pair(ref, ref), scale2 = pair(qscale[t], qscale[t]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lg[t][i] = ex2(lg[t][i] - ref);
-          l[t] += lg[t][i];
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpair(fma2(pair(lg[t][2 * i], lg[t][2 * i + 1]), scale2, ref2));
+          lg[t][2 * i] = ex2(x.x);
+          lg[t][2 * i + 1] = ex2(x.y);
+          l2[t] = add2(l2[t], pair(lg[t][2 * i], lg[t][2 * i + 1]));
         }
       }
       // O^T[d, head] += V^T[d, token] (p scale)[token, head], group by group
@@ -568,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     float* part = a.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * part_floats(G, D);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float x = l[t];
+      const float2 l = unpair(l2[t]);
+      float x = l.x + l.y;
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
       if (c == 0) {
