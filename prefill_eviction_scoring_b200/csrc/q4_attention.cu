@@ -148,6 +148,22 @@ __host__ __device__ inline size_t part_floats(int G, int D) {
   return ((size_t)G * (D + 2) + 3) / 4 * 4;
 }
 
+// V's scales of tokens 4 c .. 4 c + 3 of a half tile, groups 2 i and 2 i + 1.
+template <int D>
+__device__ inline void v_scales(const uint8_t* half, int c, int i, uint32_t (&vs)[4]) {
+  const uint8_t* at = half + 2 * Smem<D>::kCodes + Smem<D>::kScales + c * (D / 4);
+  if (D == 128) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vs[j] = *reinterpret_cast<const uint32_t*>(at + 8 * j + 4 * i);
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    vs[0] = x.x;
+    vs[1] = x.y;
+    vs[2] = x.z;
+    vs[3] = x.w;
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const DecodeArgs a) {
   constexpr int NG = D / 32, NW2 = D / 64;
@@ -429,30 +445,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
           lg[t][2 * i] = x.x;
           lg[t][2 * i + 1] = x.y;
         }
-      if (edge) {                                      // the slots past the end hold anything
+      // One test for all that is rare: slots that hold anything (past the end,
+      // no page), a maximum that lags by more than 2^kSlack, scales of V that
+      // outgrow their unit.
+      bool rare = edge;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (16 * (i / 4) + 4 * c + i % 4 >= valid || !(i < 4 ? ok.x : ok.y)) {
+      for (int t = 0; t < NT; ++t)
+        rare |= fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
+                      fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7]))) *
+                    qscale[t] > m[t] + kSlack;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) lg[t][i] = -INFINITY;
+      for (int i = 0; i < NW2; ++i) {
+        uint32_t x = limit[i];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t vs[4];
+          v_scales<D>(st + hf * S::kHalf, c, i, vs);
+          x = __vimax3_u16x2(__vimax3_u16x2(vs[0], vs[1], x), vs[2], vs[3]);
+        }
+        rare |= x != limit[i];
+      }
+      if (__any_sync(0xffffffffu, rare)) {
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (16 * (i / 4) + 4 * c + i % 4 >= valid || !(i < 4 ? ok.x : ok.y)) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t) lg[t][i] = -INFINITY;
+            }
+          // no weight: zero scales (lane: one token)
+          if (lane >= valid || !(lane < kSub ? ok.x : ok.y)) {
+            uint32_t* z = reinterpret_cast<uint32_t*>(
+                const_cast<uint8_t*>(st) + half * S::kHalf + 2 * S::kCodes + S::kScales +
+                hl * (D / 16));
+#pragma unroll
+            for (int i = 0; i < NW2; ++i) z[i] = 0;
           }
-      }
-      // the running maximum moves, and the sums with it, when it lags by 2^kSlack
-      bool move = false;
-      float top[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        top[t] = fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
-                       fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7]))) *
-                 qscale[t];
-        move |= top[t] > m[t] + kSlack;
-      }
-      if (__any_sync(0xffffffffu, move)) {
+          __syncwarp();
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 1));
-          top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], 2));
-          const float to = top[t] > m[t] + kSlack ? top[t] : m[t];
+          float top = fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
+                            fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7]))) *
+                      qscale[t];
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float to = top > m[t] + kSlack ? top : m[t];
           const float f = to == -INFINITY ? 1.f : exp2f(m[t] - to);
           m[t] = to;
           l2[t] = mul2(l2[t], pair(f, f));
@@ -464,6 +502,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
             o[t][i / 2][i % 2][1] *= f1;
             o[t][i / 2][i % 2][2] *= f0;
             o[t][i / 2][i % 2][3] *= f1;
+          }
+        }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const int sft = 16 * (gr % 2);
+          uint32_t x = 0;                              // the group's largest finite scale
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t vs[4];
+            v_scales<D>(st + hf * S::kHalf, c, gr / 2, vs);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t b = (vs[j] >> sft) & 0xffffu;
+              x = b < 0x7f80u ? max(x, b) : x;         // a NaN never fits and passes through
+            }
+          }
+          x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const uint32_t mask = 0xffffu << sft;
+          const uint32_t was = (unit[gr / 2] >> sft) & 0xffffu;
+          if (x > ((limit[gr / 2] >> sft) & 0xffffu)) {
+            int e = (int)(x >> 7) - 127;               // the largest scale in [1, 2)
+            e = e > 126 ? 126 : e;
+            const uint32_t to = (uint32_t)(127 - e) << 7;
+            const uint32_t lim = (uint32_t)min(127 + e + kScaleRoom, 254) << 7;
+            unit[gr / 2] = (unit[gr / 2] & ~mask) | (to << sft);
+            limit[gr / 2] = (limit[gr / 2] & ~mask) | (lim << sft);
+            const float f = exp2f((float)((int)(to >> 7) - (int)(was >> 7)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[t][gr][i / 4][i % 4] *= f;
           }
         }
       }
@@ -483,60 +553,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint8_t* sh = st + hf * S::kHalf;
-        uint32_t vs[4][NW2];
-#pragma unroll
-        for (int i = 0; i < NW2; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sh + 2 * S::kCodes + S::kScales +
-                                                          16 * (NW2 * c + i));
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) vs[(4 * i + j) / NW2][(4 * i + j) % NW2] = xs[j];
-        }
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (16 * hf + 4 * c + j >= valid || !(hf ? ok.y : ok.x)) {
-#pragma unroll
-              for (int i = 0; i < NW2; ++i) vs[j][i] = 0;
-            }
-        }
-        // V's scales outgrow their unit (a NaN never fits and passes through)
-        bool grow = false;
-#pragma unroll
-        for (int i = 0; i < NW2; ++i) {
-          const uint32_t x = __vimax3_u16x2(__vimax3_u16x2(vs[0][i], vs[1][i], vs[2][i]),
-                                            vs[3][i], limit[i]);
-          grow |= x != limit[i];
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            uint32_t x = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t b = (gr % 2 ? vs[j][gr / 2] >> 16 : vs[j][gr / 2]) & 0xffffu;
-              x = b < 0x7f80u ? max(x, b) : x;
-            }
-            x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            const int sft = 16 * (gr % 2);
-            const uint32_t mask = 0xffffu << sft;
-            const uint32_t was = (unit[gr / 2] >> sft) & 0xffffu;
-            if (x > ((limit[gr / 2] >> sft) & 0xffffu)) {
-              int e = (int)(x >> 7) - 127;             // the largest scale in [1, 2)
-              e = e > 126 ? 126 : e;
-              const uint32_t to = (uint32_t)(127 - e) << 7;
-              const uint32_t lim = (uint32_t)min(127 + e + kScaleRoom, 254) << 7;
-              unit[gr / 2] = (unit[gr / 2] & ~mask) | (to << sft);
-              limit[gr / 2] = (limit[gr / 2] & ~mask) | (lim << sft);
-              const float f = exp2f((float)((int)(to >> 7) - (int)(was >> 7)));
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[t][gr][i / 4][i % 4] *= f;
-            }
-          }
-        }
         uint32_t vw[4][NW2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -561,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
             e2m1_to_half(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), hi[jp]);
           }
           uint32_t sc[4];
+          v_scales<D>(sh, c, i, sc);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[j] = mul_bf16x2(vs[j][i], unit[i]);
+          for (int j = 0; j < 4; ++j) sc[j] = mul_bf16x2(sc[j], unit[i]);
 #pragma unroll
           for (int gh = 0; gh < 2; ++gh) {
             const int gr = 2 * i + gh;
