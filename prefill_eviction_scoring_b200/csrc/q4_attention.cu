@@ -31,12 +31,12 @@
 namespace waits {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
 constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
-constexpr int kCtasPerSm = 2;
+constexpr int kMinTiles = 8;          // tiles per CTA, where there are few
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
 
@@ -70,6 +70,12 @@ __device__ inline void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, ui
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The transpose of an 8 x 8 matrix of halves, a row's pairs in four lanes.
+__device__ inline uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 // Two fp32 values in one register pair.
 __device__ inline uint64_t pair(float lo, float hi) {
@@ -126,7 +132,14 @@ __device__ inline int64_t warp_sum(int64_t x) {
   return x;
 }
 
-template <int D>
+__device__ inline float max4(float a, float b, float c, float d) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return fmaxf(r, d);
+}
+
+// HEADS: query heads of a group that the kernel is built for, 4, 8 or 16.
+template <int D, int HEADS>
 struct Smem {
   static constexpr int kCodes = kSub * D / 2;           // bytes of a half tile's K (or V) codes
   static constexpr int kScales = kSub * D / 16;
@@ -134,7 +147,7 @@ struct Smem {
   static constexpr int kTileBytes = 2 * kHalf;
   static constexpr int kRow = D + 4;                    // floats per merge row, no bank conflicts
   uint8_t ring[kWarps][kStages][kTileBytes];
-  float o[kWarps][8][kRow];
+  float o[kWarps][HEADS < 8 ? HEADS : 8][kRow];
   float m[kWarps][16], l[kWarps][16];
   int32_t page_ok[kWarps][kStages][2];
   int64_t scan[kWarps];
@@ -148,31 +161,30 @@ __host__ __device__ inline size_t part_floats(int G, int D) {
   return ((size_t)G * (D + 2) + 3) / 4 * 4;
 }
 
-// V's scales of tokens 4 c .. 4 c + 3 of a half tile, groups 2 i and 2 i + 1.
-template <int D>
-__device__ inline void v_scales(const uint8_t* half, int c, int i, uint32_t (&vs)[4]) {
-  const uint8_t* at = half + 2 * Smem<D>::kCodes + Smem<D>::kScales + c * (D / 4);
-  if (D == 128) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) vs[j] = *reinterpret_cast<const uint32_t*>(at + 8 * j + 4 * i);
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(at);
-    vs[0] = x.x;
-    vs[1] = x.y;
-    vs[2] = x.z;
-    vs[3] = x.w;
-  }
+// Where part i of n of `total` units begins.
+__device__ inline int64_t split(int64_t total, int i, int n) {
+  if (total < 1 << 22) return (uint32_t)total * (uint32_t)i / (uint32_t)n;
+  return total * i / n;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const DecodeArgs a) {
-  constexpr int NG = D / 32, NW2 = D / 64;
-  using S = Smem<D>;
+// Of a warp's lanes, r = lane / 4 and c = lane % 4.  The first product has
+// tokens as rows and heads as columns, so a lane holds the logits of two
+// tokens of each half tile for heads 2 c and 2 c + 1; a transpose of the
+// scaled weights (movmatrix) makes them the second product's operand, whose
+// rows are dimensions and whose columns are the heads again.  Up to 4 heads
+// use the columns twice: 0 - 3 weigh with V's scale of the even group, 4 - 7
+// with the odd group's.
+template <int D, int HEADS>
+__global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs a) {
+  constexpr int NG = D / 32, NW2 = D / 64, NT = HEADS == 16 ? 2 : 1;
+  constexpr bool kTwice = HEADS == 4;
+  using S = Smem<D, HEADS>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int Hkv = a.c.Hkv, G = a.G, log_bs = a.c.log_bs;
+  const uint32_t group_sel = c < 2 ? 0x1044u : 0x3244u;   // a scale word's half, as fp32
   const int64_t cap = (int64_t)a.width << log_bs;
   const size_t page_bytes = Q4Page<D>::bytes(log_bs);
   pdl_allow_next();
@@ -184,15 +196,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
   };
   auto tiles = [&](int s) -> int { return (int)(((int64_t)tokens(s) + kTok - 1) / kTok); };
 
-  // empty sequences, shared among the CTAs
-  for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
-    if (tokens(s) > 0) continue;
-    for (int i = tid; i < a.Hq * D / 2; i += kThreads)
-      reinterpret_cast<uint32_t*>(a.out + (size_t)s * a.Hq * D)[i] = 0;
-    if (a.lse)
-      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)s * a.Hq + i] = -INFINITY;
-  }
-
   // total units (tiles of all items), then this CTA's run [u0, u1)
   int64_t mine = 0;
   for (int s = tid; s < a.nseq; s += kThreads) mine += tiles(s);
@@ -202,14 +205,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
   int64_t total = 0;
   for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
   total *= Hkv;
-  // one tile per warp at least
-  int64_t ctas = (total + kWarps - 1) / kWarps;
-  ctas = ctas < gridDim.x ? ctas : gridDim.x;
-  if (blockIdx.x >= ctas) {
-    if (tid == 0) a.desc[blockIdx.x].parts = 0;
+  const int ctas = total < (int64_t)kMinTiles * gridDim.x
+                       ? ((int)total + kMinTiles - 1) / kMinTiles
+                       : (int)gridDim.x;
+  if (tid == 0) a.desc[blockIdx.x].parts = 0;
+  // empty sequences, shared among the CTAs
+  auto zero_empty = [&]() {
+    for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
+      if (tokens(s) > 0) continue;
+      for (int i = tid; i < a.Hq * D / 2; i += kThreads)
+        reinterpret_cast<uint32_t*>(a.out + (size_t)s * a.Hq * D)[i] = 0;
+      if (a.lse)
+        for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)s * a.Hq + i] = -INFINITY;
+    }
+  };
+  if ((int)blockIdx.x >= ctas) {
+    zero_empty();
     return;
   }
-  const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+  const int64_t u0 = split(total, blockIdx.x, ctas), u1 = split(total, blockIdx.x + 1, ctas);
   // the sequence of u0: prefix sums, kThreads sequences at a time
   {
     int64_t before = 0;
@@ -242,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
   }
   int s = (int)sm.where[0], nt = tiles(s);
   const int64_t in_seq = u0 - sm.where[1];
-  int g = (int)(in_seq / nt), tile0 = (int)(in_seq - (int64_t)g * nt);
+  int g = in_seq >> 32 ? (int)(in_seq / nt) : (int)((uint32_t)in_seq / (uint32_t)nt);
+  int tile0 = (int)(in_seq - (int64_t)g * nt);
 
   // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..  A half warp
   // copies a half tile, whose page it looks up one tile ahead.
@@ -310,20 +325,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     cp_async_commit();
   };
   issue();
+  zero_empty();
 
   // ---- the run, item by item
   int stage = 0;
   bool first = true;
-  if (tid == 0) a.desc[blockIdx.x].parts = 0;
   for (int64_t u = u0; u < u1;) {
     const int n = tokens(s);
     const int64_t piece = u1 - u < nt - tile0 ? u1 - u : nt - tile0;
-    // Q fragments: head r (and r + 8), dimensions 16 k + 4 c .. + 3
-    uint32_t qf[NT][NG][4];    // per group: steps 0, 1 (first halves), steps 0, 1 (second halves)
-    float qscale[NT];
+    // Q fragments: column r is head r (and r + 8), dimensions 16 k + 4 c .. + 3
+    uint32_t qf[NT][D / 16][2];
+    uint64_t qscale[NT];                               // of heads 2 c, 2 c + 1
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int h = r + 8 * t;
+      const int h = (kTwice ? r & 3 : r) + 8 * t;
       uint2 raw[D / 16];
       uint32_t top = 0;
 #pragma unroll
@@ -340,18 +355,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       int e = (int)(top >> 7) - 127 - 13;              // the largest in [2^13, 2^14)
       e = e < -126 ? -126 : e;
       const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
-      qscale[t] = a.scale_log2 * exp2f((float)e);
+      const float back = a.scale_log2 * exp2f((float)e);
+      qscale[t] = pair(__shfl_sync(0xffffffffu, back, 8 * c),
+                       __shfl_sync(0xffffffffu, back, 8 * c + 4));
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        qf[t][k / 2][k % 2] = pack_half(bf16_lo(raw[k].x) * mul, bf16_hi(raw[k].x) * mul);
-        qf[t][k / 2][2 + k % 2] = pack_half(bf16_lo(raw[k].y) * mul, bf16_hi(raw[k].y) * mul);
+        qf[t][k][0] = pack_half(bf16_lo(raw[k].x) * mul, bf16_hi(raw[k].x) * mul);
+        qf[t][k][1] = pack_half(bf16_lo(raw[k].y) * mul, bf16_hi(raw[k].y) * mul);
       }
     }
-    float o[NT][NG][2][4], m[NT];
-    uint64_t l2[NT];                                   // two partial sums
+    float o[NT][NG][2][4], m[NT][2];                   // m, l: heads 2 c, 2 c + 1
+    uint64_t l2[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t] = -INFINITY;
+      m[t][0] = m[t][1] = -INFINITY;
       l2[t] = 0;
 #pragma unroll
       for (int i = 0; i < NG * 8; ++i) o[t][i / 8][i / 4 % 2][i % 4] = 0.f;
@@ -365,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     }
     int k0 = (int)(u - u0);                            // first tile of this warp in the piece
     const int kend = k0 + (int)piece, base = k0 - tile0;
-    k0 += (warp - k0) & (kWarps - 1);
+    k0 += (warp + kWarps - k0 % kWarps) % kWarps;
     for (int k = k0; k < kend; k += kWarps) {
       cp_async_wait<0>();
       __syncwarp();
@@ -375,151 +392,120 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       const int2 ok = *reinterpret_cast<const int2*>(&sm.page_ok[warp][stage][0]);
       stage ^= 1;
       const bool edge = valid < kTok || !ok.x || !ok.y;
-      // logits: S[head, token] per group, scaled by K's scales; lane: head r,
-      // tokens 4 c .. 4 c + 3 of each half
-      uint64_t lg2[NT][2][2];
+      // this lane's tokens: rows r and r + 8 of the first product
+      const int p0 = 4 * (r >> 1) + (r & 1), p1 = p0 + 2;
+      float lg[NT][2][2][2];                           // [half][token][head]
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint8_t* sh = st + hf * S::kHalf;
-        uint32_t ks[4][NW2];
-#pragma unroll
-        for (int i = 0; i < NW2; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sh + 2 * S::kCodes + 16 * (NW2 * c + i));
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ks[(4 * i + j) / NW2][(4 * i + j) % NW2] = xs[j];
+        uint32_t k0w[NG], k1w[NG], s0[NW2], s1[NW2];
+        if (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sh + p0 * 64 + 16 * c);
+          const uint4 y = *reinterpret_cast<const uint4*>(sh + p1 * 64 + 16 * c);
+          const uint2 u = *reinterpret_cast<const uint2*>(sh + 2 * S::kCodes + p0 * 8);
+          const uint2 v = *reinterpret_cast<const uint2*>(sh + 2 * S::kCodes + p1 * 8);
+          k0w[0] = x.x, k0w[1] = x.y, k0w[NG - 2] = x.z, k0w[NG - 1] = x.w;
+          k1w[0] = y.x, k1w[1] = y.y, k1w[NG - 2] = y.z, k1w[NG - 1] = y.w;
+          s0[0] = u.x, s0[NW2 - 1] = u.y;
+          s1[0] = v.x, s1[NW2 - 1] = v.y;
+        } else {
+          const int kr0 = (p0 & 9) | ((p0 & 4) >> 1), kr1 = kr0 | 4;
+          const uint2 x = *reinterpret_cast<const uint2*>(sh + kr0 * 32 + 8 * c);
+          const uint2 y = *reinterpret_cast<const uint2*>(sh + kr1 * 32 + 8 * c);
+          k0w[0] = x.x, k0w[1] = x.y;
+          k1w[0] = y.x, k1w[1] = y.y;
+          s0[0] = *reinterpret_cast<const uint32_t*>(sh + 2 * S::kCodes + p0 * 4);
+          s1[0] = *reinterpret_cast<const uint32_t*>(sh + 2 * S::kCodes + p1 * 4);
         }
 #pragma unroll
-        for (int jt = 0; jt < 2; ++jt) {
-          const int p = 4 * (r >> 1) + (r & 1) + 2 * jt;
-          uint32_t kw[NG];
-          if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(sh + p * 64 + 16 * c);
-            kw[0] = x.x;
-            kw[1] = x.y;
-            kw[NG - 2] = x.z;
-            kw[NG - 1] = x.w;
-          } else {
-            const int kr = (p & 9) | ((p & 4) >> 1) | ((p & 2) << 1);
-            const uint2 x = *reinterpret_cast<const uint2*>(sh + kr * 32 + 8 * c);
-            kw[0] = x.x;
-            kw[1] = x.y;
-          }
+        for (int gr = 0; gr < NG; ++gr) {
+          uint32_t h0[4], h1[4];
+          e2m1_to_half(k0w[gr], h0);
+          e2m1_to_half(k1w[gr], h1);
+          const float f0 = gr % 2 ? bf16_hi(s0[gr / 2]) : bf16_lo(s0[gr / 2]);
+          const float f1 = gr % 2 ? bf16_hi(s1[gr / 2]) : bf16_lo(s1[gr / 2]);
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            uint32_t h[4];
-            e2m1_to_half(kw[gr], h);
-            const uint32_t s0 = ks[2 * jt][gr / 2], s1 = ks[2 * jt + 1][gr / 2];
-            const uint64_t f =
-                gr % 2 ? pair(bf16_hi(s0), bf16_hi(s1)) : pair(bf16_lo(s0), bf16_lo(s1));
-            float acc[4], acc2[4];
-            if (NT == 1) {
-              // rows 0 - 7 of the A quad are the heads' even step, rows 8 - 15
-              // their odd step: each product is right in one half of the rows
-              mma16816_zero(acc, qf[0][gr][0], qf[0][gr][1], qf[0][gr][2], qf[0][gr][3], h[0],
-                            h[1]);
-              mma16816_zero(acc2, qf[0][gr][0], qf[0][gr][1], qf[0][gr][2], qf[0][gr][3], h[2],
-                            h[3]);
-              uint64_t& x = lg2[0][hf][jt];
-              x = gr == 0 ? mul2(pair(acc[0], acc[1]), f) : fma2(pair(acc[0], acc[1]), f, x);
-              x = fma2(pair(acc2[2], acc2[3]), f, x);
-            } else {
-              mma16816_zero(acc, qf[0][gr][0], qf[1][gr][0], qf[0][gr][2], qf[1][gr][2], h[0],
-                            h[1]);
-              mma16816(acc, qf[0][gr][1], qf[1][gr][1], qf[0][gr][3], qf[1][gr][3], h[2], h[3]);
+          for (int t = 0; t < NT; ++t) {
+            float acc[4];
+            mma16816_zero(acc, h0[0], h1[0], h0[1], h1[1], qf[t][2 * gr][0], qf[t][2 * gr][1]);
+            mma16816(acc, h0[2], h1[2], h0[3], h1[3], qf[t][2 * gr + 1][0],
+                     qf[t][2 * gr + 1][1]);
 #pragma unroll
-              for (int t = 0; t < NT; ++t) {
-                const uint64_t x = pair(acc[2 * t], acc[2 * t + 1]);
-                lg2[t][hf][jt] = gr == 0 ? mul2(x, f) : fma2(x, f, lg2[t][hf][jt]);
-              }
+            for (int b = 0; b < 2; ++b) {
+              float &x = lg[t][hf][0][b], &y = lg[t][hf][1][b];
+              x = gr == 0 ? acc[b] * f0 : fmaf(acc[b], f0, x);
+              y = gr == 0 ? acc[2 + b] * f1 : fmaf(acc[2 + b], f1, y);
             }
           }
         }
       }
-      float lg[NT][8];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = unpair(lg2[t][i / 2][i % 2]);
-          lg[t][2 * i] = x.x;
-          lg[t][2 * i + 1] = x.y;
-        }
       // One test for all that is rare: slots that hold anything (past the end,
       // no page), a maximum that lags by more than 2^kSlack, scales of V that
       // outgrow their unit.
       bool rare = edge;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        rare |= fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
-                      fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7]))) *
-                    qscale[t] > m[t] + kSlack;
+      for (int t = 0; t < NT; ++t) {
+        const float2 qs = unpair(qscale[t]);
 #pragma unroll
-      for (int i = 0; i < NW2; ++i) {
-        uint32_t x = limit[i];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t vs[4];
-          v_scales<D>(st + hf * S::kHalf, c, i, vs);
-          x = __vimax3_u16x2(__vimax3_u16x2(vs[0], vs[1], x), vs[2], vs[3]);
+        for (int b = 0; b < 2; ++b)
+          rare |= max4(lg[t][0][0][b], lg[t][0][1][b], lg[t][1][0][b], lg[t][1][1][b]) *
+                      (b ? qs.y : qs.x) > m[t][b] + kSlack;
+      }
+      {                                                // lane: the scales of one token
+        const uint8_t* at = st + half * S::kHalf + 2 * S::kCodes + S::kScales + hl * (D / 16);
+        if (D == 128) {
+          const uint2 x = *reinterpret_cast<const uint2*>(at);
+          rare |= __vmaxu2(x.x, limit[0]) != limit[0] ||
+                  __vmaxu2(x.y, limit[NW2 - 1]) != limit[NW2 - 1];
+        } else {
+          rare |= __vmaxu2(*reinterpret_cast<const uint32_t*>(at), limit[0]) != limit[0];
         }
-        rare |= x != limit[i];
       }
       if (__any_sync(0xffffffffu, rare)) {
+        uint32_t* own = reinterpret_cast<uint32_t*>(
+            const_cast<uint8_t*>(st) + half * S::kHalf + 2 * S::kCodes + S::kScales +
+            hl * (D / 16));
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (16 * (i / 4) + 4 * c + i % 4 >= valid || !(i < 4 ? ok.x : ok.y)) {
+          for (int i = 0; i < 4; ++i)
+            if (16 * (i / 2) + (i % 2 ? p1 : p0) >= valid || !(i < 2 ? ok.x : ok.y)) {
 #pragma unroll
-              for (int t = 0; t < NT; ++t) lg[t][i] = -INFINITY;
+              for (int t = 0; t < NT; ++t)
+                lg[t][i / 2][i % 2][0] = lg[t][i / 2][i % 2][1] = -INFINITY;
             }
           // no weight: zero scales (lane: one token)
           if (lane >= valid || !(lane < kSub ? ok.x : ok.y)) {
-            uint32_t* z = reinterpret_cast<uint32_t*>(
-                const_cast<uint8_t*>(st) + half * S::kHalf + 2 * S::kCodes + S::kScales +
-                hl * (D / 16));
 #pragma unroll
-            for (int i = 0; i < NW2; ++i) z[i] = 0;
+            for (int i = 0; i < NW2; ++i) own[i] = 0;
           }
           __syncwarp();
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float top = fmaxf(fmaxf(fmaxf(lg[t][0], lg[t][1]), fmaxf(lg[t][2], lg[t][3])),
-                            fmaxf(fmaxf(lg[t][4], lg[t][5]), fmaxf(lg[t][6], lg[t][7]))) *
-                      qscale[t];
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float to = top > m[t] + kSlack ? top : m[t];
-          const float f = to == -INFINITY ? 1.f : exp2f(m[t] - to);
-          m[t] = to;
-          l2[t] = mul2(l2[t], pair(f, f));
-          const float f0 = __shfl_sync(0xffffffffu, f, 8 * c);
-          const float f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+          const float2 qs = unpair(qscale[t]);
+          float f[2];
 #pragma unroll
-          for (int i = 0; i < NG * 2; ++i) {
-            o[t][i / 2][i % 2][0] *= f0;
-            o[t][i / 2][i % 2][1] *= f1;
-            o[t][i / 2][i % 2][2] *= f0;
-            o[t][i / 2][i % 2][3] *= f1;
+          for (int b = 0; b < 2; ++b) {
+            float top = max4(lg[t][0][0][b], lg[t][0][1][b], lg[t][1][0][b], lg[t][1][1][b]) *
+                        (b ? qs.y : qs.x);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float to = top > m[t][b] + kSlack ? top : m[t][b];
+            f[b] = to == -INFINITY ? 1.f : exp2f(m[t][b] - to);
+            m[t][b] = to;
           }
+          l2[t] = mul2(l2[t], pair(f[0], f[1]));
+#pragma unroll
+          for (int i = 0; i < NG * 8; ++i) o[t][i / 8][i / 4 % 2][i % 4] *= f[i % 2];
         }
+        // the groups' largest finite scales (a NaN never fits and passes through)
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           const int sft = 16 * (gr % 2);
-          uint32_t x = 0;                              // the group's largest finite scale
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t vs[4];
-            v_scales<D>(st + hf * S::kHalf, c, gr / 2, vs);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t b = (vs[j] >> sft) & 0xffffu;
-              x = b < 0x7f80u ? max(x, b) : x;         // a NaN never fits and passes through
-            }
-          }
-          x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          uint32_t x = (own[gr / 2] >> sft) & 0xffffu;
+          x = x < 0x7f80u ? x : 0;
+          x = __reduce_max_sync(0xffffffffu, x);
           const uint32_t mask = 0xffffu << sft;
           const uint32_t was = (unit[gr / 2] >> sft) & 0xffffu;
           if (x > ((limit[gr / 2] >> sft) & 0xffffu)) {
@@ -539,23 +525,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float ref = m[t] == -INFINITY ? 0.f : -m[t];
-        const uint64_t ref2 = pair(ref, ref), scale2 = pair(qscale[t], qscale[t]);
+        const uint64_t ref = pair(m[t][0] == -INFINITY ? 0.f : -m[t][0],
+                                  m[t][1] == -INFINITY ? 0.f : -m[t][1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 x = unpair(fma2(pair(lg[t][2 * i], lg[t][2 * i + 1]), scale2, ref2));
-          lg[t][2 * i] = ex2(x.x);
-          lg[t][2 * i + 1] = ex2(x.y);
-          l2[t] = add2(l2[t], pair(lg[t][2 * i], lg[t][2 * i + 1]));
+          float(&x)[2] = lg[t][i / 2][i % 2];
+          const float2 y = unpair(fma2(pair(x[0], x[1]), qscale[t], ref));
+          x[0] = ex2(y.x);
+          x[1] = ex2(y.y);
+          l2[t] = add2(l2[t], pair(x[0], x[1]));
         }
       }
       // O^T[d, head] += V^T[d, token] (p scale)[token, head], group by group
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint8_t* sh = st + hf * S::kHalf;
-        uint32_t vw[4][NW2];
+        const uint8_t* sc = sh + 2 * S::kCodes + S::kScales;
+        uint32_t s0[NW2], s1[NW2], vw[4][NW2];
+        if (D == 128) {
+          const uint2 u = *reinterpret_cast<const uint2*>(sc + p0 * 8);
+          const uint2 v = *reinterpret_cast<const uint2*>(sc + p1 * 8);
+          s0[0] = u.x, s0[NW2 - 1] = u.y;
+          s1[0] = v.x, s1[NW2 - 1] = v.y;
+        } else {
+          s0[0] = *reinterpret_cast<const uint32_t*>(sc + p0 * 4);
+          s1[0] = *reinterpret_cast<const uint32_t*>(sc + p1 * 4);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j) {                  // V's rows of tokens 4 c + j
           if (D == 128) {
             const uint2 x = *reinterpret_cast<const uint2*>(
                 sh + S::kCodes + (4 * j + c) * 64 + (((r >> 1) ^ (2 * (c >> 1))) * 16) +
@@ -563,41 +560,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
             vw[j][0] = x.x;
             vw[j][NW2 - 1] = x.y;
           } else {
-            vw[j][0] = *reinterpret_cast<const uint32_t*>(sh + S::kCodes + (4 * j + c) * 32 + 4 * r);
+            vw[j][0] =
+                *reinterpret_cast<const uint32_t*>(sh + S::kCodes + (4 * j + c) * 32 + 4 * r);
           }
         }
 #pragma unroll
         for (int i = 0; i < NW2; ++i) {
+          const uint32_t w0 = mul_bf16x2(s0[i], unit[i]), w1 = mul_bf16x2(s1[i], unit[i]);
+          uint32_t b[NT][2][2];                        // [group of the pair][token pair]
+#pragma unroll
+          for (int gh = 0; gh < 2; ++gh) {
+            if (kTwice && gh) continue;
+            float f0, f1;
+            if (kTwice) {                              // this column's group
+              f0 = __uint_as_float(__byte_perm(w0, 0, group_sel));
+              f1 = __uint_as_float(__byte_perm(w1, 0, group_sel));
+            } else {
+              f0 = gh ? bf16_hi(w0) : bf16_lo(w0);
+              f1 = gh ? bf16_hi(w1) : bf16_lo(w1);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const float(&x)[2][2] = lg[t][hf];
+              b[t][gh][0] = transpose8(pack_half(x[0][0] * f0, x[0][1] * f0));
+              b[t][gh][1] = transpose8(pack_half(x[1][0] * f1, x[1][1] * f1));
+            }
+          }
           // tokens j, j + 1 of one dimension into one byte; even, odd dimensions
           uint32_t lo[2][4], hi[2][4];
 #pragma unroll
           for (int jp = 0; jp < 2; ++jp) {
-            const uint32_t w0 = vw[2 * jp][i], w1 = vw[2 * jp + 1][i];
-            e2m1_to_half((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), lo[jp]);
-            e2m1_to_half(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), hi[jp]);
+            const uint32_t x = vw[2 * jp][i], y = vw[2 * jp + 1][i];
+            e2m1_to_half((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), lo[jp]);
+            e2m1_to_half(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), hi[jp]);
           }
-          uint32_t sc[4];
-          v_scales<D>(sh, c, i, sc);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[j] = mul_bf16x2(sc[j], unit[i]);
+          for (int gh = 0; gh < 2; ++gh)
 #pragma unroll
-          for (int gh = 0; gh < 2; ++gh) {
-            const int gr = 2 * i + gh;
-            const uint64_t f01 = gh ? pair(bf16_hi(sc[0]), bf16_hi(sc[1]))
-                                    : pair(bf16_lo(sc[0]), bf16_lo(sc[1]));
-            const uint64_t f23 = gh ? pair(bf16_hi(sc[2]), bf16_hi(sc[3]))
-                                    : pair(bf16_lo(sc[2]), bf16_lo(sc[3]));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const float2 x = unpair(mul2(pair(lg[t][4 * hf], lg[t][4 * hf + 1]), f01));
-              const float2 y = unpair(mul2(pair(lg[t][4 * hf + 2], lg[t][4 * hf + 3]), f23));
-              const uint32_t b0 = pack_half(x.x, x.y), b1 = pack_half(y.x, y.y);
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt)
-                mma16816(o[t][gr][mt], lo[0][2 * gh + mt], hi[0][2 * gh + mt], lo[1][2 * gh + mt],
-                         hi[1][2 * gh + mt], b0, b1);
-            }
-          }
+                mma16816(o[t][2 * i + gh][mt], lo[0][2 * gh + mt], hi[0][2 * gh + mt],
+                         lo[1][2 * gh + mt], hi[1][2 * gh + mt], b[t][kTwice ? 0 : gh][0],
+                         b[t][kTwice ? 0 : gh][1]);
         }
       }
     }
@@ -606,13 +611,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     float* part = a.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * part_floats(G, D);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float2 l = unpair(l2[t]);
-      float x = l.x + l.y;
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      if (c == 0) {
-        sm.m[warp][r + 8 * t] = m[t];
-        sm.l[warp][r + 8 * t] = x;
+      float2 l = unpair(l2[t]);
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l.x += __shfl_xor_sync(0xffffffffu, l.x, x);
+        l.y += __shfl_xor_sync(0xffffffffu, l.y, x);
+      }
+      if (r == 0 && (!kTwice || c < 2)) {
+        *reinterpret_cast<float2*>(&sm.m[warp][2 * c + 8 * t]) = make_float2(m[t][0], m[t][1]);
+        *reinterpret_cast<float2*>(&sm.l[warp][2 * c + 8 * t]) = l;
       }
     }
     __syncthreads();
@@ -620,19 +627,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int h = 2 * c + b;
+        const int h = 2 * (kTwice ? c & 1 : c) + b;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][h + 8 * t]);
-        const float mw = sm.m[warp][h + 8 * t];
-        const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+        const float f = m[t][b] == -INFINITY ? 0.f : exp2f(m[t][b] - M);
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const uint32_t un = (unit[gr / 2] >> (16 * (gr % 2) + 7)) & 0xffu;
+        for (int gr = 0; gr < NG; gr += kTwice ? 2 : 1) {
+          const bool odd = kTwice && c >= 2;           // this column's group
+          const uint32_t un = (unit[gr / 2] >> (kTwice ? (odd ? 23 : 7) : 16 * (gr % 2) + 7)) & 0xffu;
           const float v = exp2f((float)(127 - (int)un));
-          *reinterpret_cast<float4*>(&sm.o[warp][h][32 * gr + 4 * r]) =
-              make_float4(o[t][gr][0][b] * v * f, o[t][gr][0][2 + b] * v * f,
-                          o[t][gr][1][b] * v * f, o[t][gr][1][2 + b] * v * f);
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = (odd ? o[t][kTwice ? gr + 1 : gr][i / 2][2 * (i % 2) + b]
+                        : o[t][gr][i / 2][2 * (i % 2) + b]) * v * f;
+          *reinterpret_cast<float4*>(&sm.o[warp][h][32 * (gr + odd) + 4 * r]) =
+              make_float4(x[0], x[1], x[2], x[3]);
         }
       }
       __syncthreads();
@@ -674,7 +685,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
     // the first part of an item that goes on in the next CTAs
     if (!whole && tile0 == 0 && tid == 0) {
       const int64_t end = u + nt;                      // where the item ends; its last CTA
-      const int64_t last = (end * ctas - 1) / total;
+      const int64_t last = end < 1 << 22 ? ((uint32_t)end * (uint32_t)ctas - 1) / (uint32_t)total
+                                         : (end * ctas - 1) / total;
       a.desc[blockIdx.x] = Desc{s, g, (int32_t)(last - blockIdx.x + 1), first ? 0 : 1};
     }
     u += piece;
@@ -688,46 +700,87 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) q4_decode_kernel(const D
   cp_async_wait<0>();
 }
 
-// Joins the parts of an item: grid (CTAs of the first kernel, G), D threads.
+// Joins the parts of an item: a CTA per CTA of the first kernel, a warp per
+// head.  A lane takes the maximum and sum of every 32nd part, then the warp
+// adds up the weighted sums in order, a lane D / 32 dimensions.
 template <int D>
-__global__ void __launch_bounds__(D) q4_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(512) q4_join_kernel(const DecodeArgs a) {
+  constexpr int kE = D / 32;
   pdl_allow_next();
   pdl_wait();
   const Desc de = a.desc[blockIdx.x];
   if (de.parts == 0) return;
-  const int h = blockIdx.y, t = threadIdx.x, G = a.G;
+  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G;
   const size_t stride = part_floats(G, D);
   // part 0 in this CTA's slot, the others in the first slots of the next CTAs
   auto at = [&](int i) {
     return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? de.slot : 0)) * stride;
   };
-  float M = -INFINITY;
-  for (int i = 0; i < de.parts; ++i) M = fmaxf(M, at(i)[(size_t)G * D + h]);
-  float L = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < de.parts; ++i) {
-    const float* p = at(i);
-    const float m = p[(size_t)G * D + h];
-    const float f = m == -INFINITY ? 0.f : exp2f(m - M);
-    L = fmaf(p[(size_t)G * D + G + h], f, L);
-    acc = fmaf(p[(size_t)h * D + t], f, acc);
+  float M = -INFINITY, L = 0.f, acc[kE] = {};
+  for (int i0 = 0; i0 < de.parts; i0 += 32) {
+    const int n = de.parts - i0 < 32 ? de.parts - i0 : 32;
+    float m = -INFINITY, l = 0.f;
+    if (lane < n) {
+      m = at(i0 + lane)[(size_t)G * D + h];
+      l = at(i0 + lane)[(size_t)G * D + G + h];
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, M);
+    const float back = M == -INFINITY ? 0.f : exp2f(M - top);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+    M = top;
+    l *= f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L = L * back + l;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] *= back;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      const float* x = at(i0 + i) + (size_t)h * D + kE * lane;
+      if (kE == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(x);
+        acc[0] = fmaf(y.x, w, acc[0]);
+        acc[1] = fmaf(y.y, w, acc[1]);
+        acc[kE - 2] = fmaf(y.z, w, acc[kE - 2]);
+        acc[kE - 1] = fmaf(y.w, w, acc[kE - 1]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(x);
+        acc[0] = fmaf(y.x, w, acc[0]);
+        acc[1] = fmaf(y.y, w, acc[1]);
+      }
+    }
   }
   const size_t row = (size_t)de.s * a.Hq + (size_t)de.g * G + h;
-  const float v = L == 0.f ? 0.f : acc / L;
-  a.out[row * D + t] = (uint16_t)(pack_bf16(v, 0.f) & 0xffffu);
-  if (a.lse && t == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int e = 0; e < kE; e += 2)
+    *reinterpret_cast<uint32_t*>(a.out + row * D + kE * lane + e) =
+        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// The CTAs that the workspace has room for: every SM of a B200, twice.
-constexpr int kMaxCtas = 148 * kCtasPerSm;
+// The CTAs that the workspace has room for: one on every SM of a B200.
+constexpr int kMaxCtas = 148;
 
-template <int D, int NT>
+template <int D, int HEADS>
 cudaError_t launch_d(const DecodeArgs& a, int dev, int ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, NT>, dim3(ctas),
-                                          dim3(kThreads), sizeof(Smem<D>), st, a);
+  const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, HEADS>, dim3(ctas),
+                                          dim3(kThreads), sizeof(Smem<D, HEADS>), st, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(q4_join_kernel<D>, dim3(ctas, a.G), dim3(D), 0, st, a);
+  return launch_pdl(q4_join_kernel<D>, dim3(ctas), dim3(32 * a.G), 0, st, a);
+}
+
+template <int D>
+cudaError_t launch_heads(const DecodeArgs& a, int dev, int ctas, cudaStream_t st) {
+  return a.G <= 4   ? launch_d<D, 4>(a, dev, ctas, st)
+         : a.G <= 8 ? launch_d<D, 8>(a, dev, ctas, st)
+                    : launch_d<D, 16>(a, dev, ctas, st);
 }
 
 }  // namespace
@@ -742,14 +795,12 @@ cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const
   int dev = 0, sms = 0;
   const cudaError_t err = current_sms(&dev, &sms);
   if (err != cudaSuccess) return err;
-  const int ctas = sms * kCtasPerSm < kMaxCtas ? sms * kCtasPerSm : kMaxCtas;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   Desc* desc = static_cast<Desc*>(ws);
   const DecodeArgs a{c, nseq, Hq, Hq / c.Hkv, width, q, table, len, out, lse,
                      reinterpret_cast<float*>(desc + kMaxCtas), desc, status,
                      (float)(1.4426950408889634 / std::sqrt((double)c.d))};
-  const bool wide = a.G > 8;
-  if (c.d == 64) return wide ? launch_d<64, 2>(a, dev, ctas, st) : launch_d<64, 1>(a, dev, ctas, st);
-  return wide ? launch_d<128, 2>(a, dev, ctas, st) : launch_d<128, 1>(a, dev, ctas, st);
+  return c.d == 64 ? launch_heads<64>(a, dev, ctas, st) : launch_heads<128>(a, dev, ctas, st);
 }
 
 }  // namespace waits
