@@ -37,6 +37,7 @@ constexpr int kSub = 16;              // tokens of one mma step; a page is a mul
 constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
 constexpr int kMinTiles = 8;          // tiles per CTA, where there are few
+constexpr int kEndTiles = 20;         // the end of an item inside a run, in tiles of a CTA
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
 
@@ -161,10 +162,20 @@ __host__ __device__ inline size_t part_floats(int G, int D) {
   return ((size_t)G * (D + 2) + 3) / 4 * 4;
 }
 
-// Where part i of n of `total` units begins.
+// Where part i of n of `total` tiles begins.
 __device__ inline int64_t split(int64_t total, int i, int n) {
   if (total < 1 << 22) return (uint32_t)total * (uint32_t)i / (uint32_t)n;
   return total * i / n;
+}
+
+// The CTAs that share `total` tiles, kMinTiles each at least.
+__device__ inline int stream_ctas(int64_t total, int grid) {
+  return total < (int64_t)kMinTiles * grid ? ((int)total + kMinTiles - 1) / kMinTiles : grid;
+}
+// Whose run has tile `unit`.
+__device__ inline int cta_of(int64_t unit, int64_t total, int ctas) {
+  if (total < 1 << 22) return (((uint32_t)unit + 1) * (uint32_t)ctas - 1) / (uint32_t)total;
+  return (int)(((unit + 1) * ctas - 1) / total);
 }
 
 // Of a warp's lanes, r = lane / 4 and c = lane % 4.  The first product has
@@ -196,18 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
   };
   auto tiles = [&](int s) -> int { return (int)(((int64_t)tokens(s) + kTok - 1) / kTok); };
 
-  // total units (tiles of all items), then this CTA's run [u0, u1)
-  int64_t mine = 0;
-  for (int s = tid; s < a.nseq; s += kThreads) mine += tiles(s);
-  mine = warp_sum(mine);
-  if (lane == 0) sm.scan[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
-  total *= Hkv;
-  const int ctas = total < (int64_t)kMinTiles * gridDim.x
-                       ? ((int)total + kMinTiles - 1) / kMinTiles
-                       : (int)gridDim.x;
   if (tid == 0) a.desc[blockIdx.x].parts = 0;
   // empty sequences, shared among the CTAs
   auto zero_empty = [&]() {
@@ -219,50 +218,119 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
         for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)s * a.Hq + i] = -INFINITY;
     }
   };
-  if ((int)blockIdx.x >= ctas) {
-    zero_empty();
-    return;
-  }
-  const int64_t u0 = split(total, blockIdx.x, ctas), u1 = split(total, blockIdx.x + 1, ctas);
-  // the sequence of u0: prefix sums, kThreads sequences at a time
-  {
+  // This CTA's run: `run` tiles from tile0 of item (s, g) on, which has nt.
+  int s, g, tile0, nt;
+  int64_t run, total = 0, u0 = 0;          // u0: tiles before the run
+  int ctas = 0, parts = 0;                 // parts: CTAs per item, 0 where runs cross items
+  const int grid = gridDim.x, me = blockIdx.x;
+  if (a.nseq <= 32) {
+    // every warp by itself, a lane per sequence
+    const int mine = lane < a.nseq ? tiles(lane) : 0;
+    const int items = __popc(__ballot_sync(0xffffffffu, mine > 0)) * Hkv;
+    total = warp_sum((int64_t)mine) * Hkv;
+    // Whole CTAs per item, where that lengthens the longest run by less than
+    // the end of an item inside a run costs.
+    const bool apart = total > 0 && 2 * items <= grid &&
+                       total * items < (int64_t)kEndTiles * grid * (grid - items);
+    int per = 1;                           // CTAs per item of this lane's sequence
+    if (apart) {
+      const int most = max((int)((total + grid - items - 1) / (grid - items)), kMinTiles);
+      per = (mine + most - 1) / most;
+    }
+    ctas = stream_ctas(total, grid);
+    u0 = apart || me >= ctas ? me : split(total, me, ctas);
+    const int64_t x = (int64_t)(apart ? per : mine) * Hkv;
+    int64_t upto = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, u0 < upto);
+    if (here == 0 || (!apart && me >= ctas)) {
+      zero_empty();
+      return;
+    }
+    s = __ffs(here) - 1;
+    nt = __shfl_sync(0xffffffffu, mine, s);
+    const int64_t in_seq = u0 - __shfl_sync(0xffffffffu, upto - x, s);
+    if (apart) {
+      parts = __shfl_sync(0xffffffffu, per, s);
+      g = (int)in_seq / parts;
+      const int i = (int)in_seq - g * parts;
+      tile0 = (int)split(nt, i, parts);
+      run = split(nt, i + 1, parts) - tile0;
+    } else {
+      g = in_seq >> 32 ? (int)(in_seq / nt) : (int)((uint32_t)in_seq / (uint32_t)nt);
+      tile0 = (int)(in_seq - (int64_t)g * nt);
+      run = split(total, me + 1, ctas) - u0;
+    }
+  } else {
+    int64_t mine = 0;
+    for (int i = tid; i < a.nseq; i += kThreads) mine += tiles(i);
+    mine = warp_sum(mine);
+    if (lane == 0) sm.scan[warp] = mine;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
+    total *= Hkv;
+    ctas = stream_ctas(total, grid);
+    if (me >= ctas) {
+      zero_empty();
+      return;
+    }
+    u0 = split(total, me, ctas);
+    run = split(total, me + 1, ctas) - u0;
+    // the sequence of u0: prefix sums, kThreads sequences at a time
     int64_t before = 0;
-    for (int s0 = 0;; s0 += kThreads) {
-      const int s = s0 + tid;
-      const int64_t t = s < a.nseq ? (int64_t)tiles(s) * Hkv : 0;
-      int64_t x = t;
+    for (int s0 = 0; before <= u0; s0 += kThreads) {
+      const int64_t x = s0 + tid < a.nseq ? (int64_t)tiles(s0 + tid) * Hkv : 0;
+      int64_t upto = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
       __syncthreads();
-      if (lane == 31) sm.scan[warp] = x;
+      if (lane == 31) sm.scan[warp] = upto;
       __syncthreads();
       int64_t sum = 0;
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) x += sm.scan[w];
+        if (w < warp) upto += sm.scan[w];
         sum += sm.scan[w];
       }
-      x += before;
-      if (t > 0 && x - t <= u0 && u0 < x) {
-        sm.where[0] = s;
-        sm.where[1] = x - t;
+      upto += before;
+      if (upto - x <= u0 && u0 < upto) {
+        sm.where[0] = s0 + tid;
+        sm.where[1] = u0 - (upto - x);
       }
       before += sum;
-      if (before > u0) break;
     }
     __syncthreads();
+    s = (int)sm.where[0];
+    nt = tiles(s);
+    g = (int)(sm.where[1] / nt);
+    tile0 = (int)(sm.where[1] - (int64_t)g * nt);
   }
-  int s = (int)sm.where[0], nt = tiles(s);
-  const int64_t in_seq = u0 - sm.where[1];
-  int g = in_seq >> 32 ? (int)(in_seq / nt) : (int)((uint32_t)in_seq / (uint32_t)nt);
-  int tile0 = (int)(in_seq - (int64_t)g * nt);
+  // Q's fragments: column r is head r (and r + 8), dimensions 16 k + 4 c .. + 3
+  uint2 raw[NT][D / 16];
+  auto load_q = [&](int s, int g) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int h = (kTwice ? r & 3 : r) + 8 * t;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        raw[t][k] = make_uint2(0, 0);
+        if (h < G)
+          raw[t][k] = __ldg(reinterpret_cast<const uint2*>(
+              a.q + ((size_t)s * a.Hq + (size_t)g * G + h) * D + 16 * k + 4 * c));
+      }
+    }
+  };
 
   // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..  A half warp
   // copies a half tile, whose page it looks up one tile ahead.
   int p_left = 0;                          // tiles not yet issued
-  if (u1 - u0 > warp) p_left = (int)((u1 - u0 - warp + kWarps - 1) / kWarps);
+  if (run > warp) p_left = (int)((run - warp + kWarps - 1) / kWarps);
   int p_s = s, p_g = g, p_nt = nt, p_tile = tile0, p_stage = 0, p_block = -1;
   const int half = lane >> 4, hl = lane & 15;
   auto settle = [&]() {                    // bring p_tile into its item; load the half's block
@@ -324,32 +392,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
     }
     cp_async_commit();
   };
+  load_q(s, g);
   issue();
   zero_empty();
 
   // ---- the run, item by item
   int stage = 0;
   bool first = true;
-  for (int64_t u = u0; u < u1;) {
+  const int run_tiles = (int)run;
+  for (int u = 0; u < run_tiles;) {
     const int n = tokens(s);
-    const int64_t piece = u1 - u < nt - tile0 ? u1 - u : nt - tile0;
-    // Q fragments: column r is head r (and r + 8), dimensions 16 k + 4 c .. + 3
+    const int piece = min(run_tiles - u, nt - tile0);
     uint32_t qf[NT][D / 16][2];
     uint64_t qscale[NT];                               // of heads 2 c, 2 c + 1
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int h = (kTwice ? r & 3 : r) + 8 * t;
-      uint2 raw[D / 16];
       uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        raw[k] = make_uint2(0, 0);
-        if (h < G)
-          raw[k] = __ldg(reinterpret_cast<const uint2*>(
-              a.q + ((size_t)s * a.Hq + (size_t)g * G + h) * D + 16 * k + 4 * c));
-        top = max(top, max(max(raw[k].x & 0x7fffu, (raw[k].x >> 16) & 0x7fffu),
-                           max(raw[k].y & 0x7fffu, (raw[k].y >> 16) & 0x7fffu)));
-      }
+      for (int k = 0; k < D / 16; ++k)
+        top = max(top, max(max(raw[t][k].x & 0x7fffu, (raw[t][k].x >> 16) & 0x7fffu),
+                           max(raw[t][k].y & 0x7fffu, (raw[t][k].y >> 16) & 0x7fffu)));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int e = (int)(top >> 7) - 127 - 13;              // the largest in [2^13, 2^14)
@@ -360,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
                        __shfl_sync(0xffffffffu, back, 8 * c + 4));
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        qf[t][k][0] = pack_half(bf16_lo(raw[k].x) * mul, bf16_hi(raw[k].x) * mul);
-        qf[t][k][1] = pack_half(bf16_lo(raw[k].y) * mul, bf16_hi(raw[k].y) * mul);
+        qf[t][k][0] = pack_half(bf16_lo(raw[t][k].x) * mul, bf16_hi(raw[t][k].x) * mul);
+        qf[t][k][1] = pack_half(bf16_lo(raw[t][k].y) * mul, bf16_hi(raw[t][k].y) * mul);
       }
     }
     float o[NT][NG][2][4], m[NT][2];                   // m, l: heads 2 c, 2 c + 1
@@ -380,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
       unit[i] = 0x7e807e80u;                           // 2^126
       limit[i] = 0x03800380u;                          // 2^-120
     }
-    int k0 = (int)(u - u0);                            // first tile of this warp in the piece
-    const int kend = k0 + (int)piece, base = k0 - tile0;
+    int k0 = u;                                        // first tile of this warp in the piece
+    const int kend = u + piece, base = u - tile0;
     k0 += (warp + kWarps - k0 % kWarps) % kWarps;
     for (int k = k0; k < kend; k += kWarps) {
       cp_async_wait<0>();
@@ -606,7 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
         }
       }
     }
-    // ---- the item's end: join the warps' sums
+    // ---- the item's end: join the warps' sums, the next item's queries on the way
+    int next_s = s, next_g = g, next_nt = nt;
+    if (u + piece < run_tiles) {
+      if (++next_g == Hkv) {
+        next_g = 0;
+        do ++next_s; while ((next_nt = tiles(next_s)) == 0);
+      }
+      load_q(next_s, next_g);
+    }
     const bool whole = piece == nt;
     float* part = a.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * part_floats(G, D);
 #pragma unroll
@@ -684,18 +754,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
     }
     // the first part of an item that goes on in the next CTAs
     if (!whole && tile0 == 0 && tid == 0) {
-      const int64_t end = u + nt;                      // where the item ends; its last CTA
-      const int64_t last = end < 1 << 22 ? ((uint32_t)end * (uint32_t)ctas - 1) / (uint32_t)total
-                                         : (end * ctas - 1) / total;
-      a.desc[blockIdx.x] = Desc{s, g, (int32_t)(last - blockIdx.x + 1), first ? 0 : 1};
+      const int all = parts ? parts : cta_of(u0 + u + nt - 1, total, ctas) - me + 1;
+      a.desc[me] = Desc{s, g, all, first ? 0 : 1};
     }
     u += piece;
     tile0 = 0;
     first = false;
-    if (u < u1 && ++g == Hkv) {
-      g = 0;
-      do ++s; while ((nt = tiles(s)) == 0);
-    }
+    s = next_s;
+    g = next_g;
+    nt = next_nt;
   }
   cp_async_wait<0>();
 }
@@ -708,10 +775,10 @@ __global__ void __launch_bounds__(512) q4_join_kernel(const DecodeArgs a) {
   constexpr int kE = D / 32;
   pdl_allow_next();
   pdl_wait();
-  const Desc de = a.desc[blockIdx.x];
-  if (de.parts == 0) return;
   const int h = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G;
   const size_t stride = part_floats(G, D);
+  const Desc de = a.desc[blockIdx.x];
+  if (de.parts == 0) return;
   // part 0 in this CTA's slot, the others in the first slots of the next CTAs
   auto at = [&](int i) {
     return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? de.slot : 0)) * stride;
