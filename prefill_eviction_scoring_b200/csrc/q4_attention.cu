@@ -27,11 +27,13 @@
 // fp16 (2^-11 relative; bf16 would give 2^-8), after a power of two per warp
 // and group keeps them below 2^14 and V's largest scale near 1.
 #include "q4.cuh"
+#include "sm100.cuh"
 
 namespace waits {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;
+constexpr int kJoiners = 4;           // warps that add up an item's sums, in turn
 constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
 constexpr int kTok = 2 * kSub;        // tokens per tile
@@ -148,8 +150,10 @@ struct Smem {
   static constexpr int kTileBytes = 2 * kHalf;
   static constexpr int kRow = D + 4;                    // floats per merge row, no bank conflicts
   uint8_t ring[kWarps][kStages][kTileBytes];
-  float o[kWarps][HEADS < 8 ? HEADS : 8][kRow];
-  float m[kWarps][16], l[kWarps][16];
+  static constexpr int kSlots = HEADS == 16 ? 1 : 2;    // items whose ends may overlap
+  float o[kSlots][kWarps][HEADS][kRow];
+  float m[kSlots][kWarps][HEADS], l[kSlots][kWarps][HEADS];
+  uint64_t full[kSlots], free[kSlots];
   int32_t page_ok[kWarps][kStages][2];
   int64_t scan[kWarps];
   int64_t total;
@@ -166,6 +170,19 @@ __host__ __device__ inline size_t part_floats(int G, int D) {
 __device__ inline int64_t split(int64_t total, int i, int n) {
   if (total < 1 << 22) return (uint32_t)total * (uint32_t)i / (uint32_t)n;
   return total * i / n;
+}
+
+// Waits for a phase of a barrier in shared memory: all its arrivals are this
+// CTA's own.  Bounded: after 2 s the warp flags the status and gives up.
+__device__ inline bool wait_for(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  bool ok = sm100::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = sm100::globaltimer();
+    while (!(ok = sm100::mbar_try_wait(bar, parity)) && sm100::globaltimer() - t0 < 2000000000ull) {
+    }
+    if (!ok && status) atomicOr(status, WAITS_DEV_TIMEOUT);
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // The CTAs that share `total` tiles, kMinTiles each at least.
@@ -198,6 +215,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
   const uint32_t group_sel = c < 2 ? 0x1044u : 0x3244u;   // a scale word's half, as fp32
   const int64_t cap = (int64_t)a.width << log_bs;
   const size_t page_bytes = Q4Page<D>::bytes(log_bs);
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      sm100::mbar_init(&sm.full[i], kWarps);
+      sm100::mbar_init(&sm.free[i], kJoiners);
+    }
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
   pdl_allow_next();
   pdl_wait();
 
@@ -384,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
       } else if (a.status && p_block != -2 && hl == 0) {
         atomicOr(a.status, WAITS_DEV_BAD_INDEX);
       }
-      p_stage ^= 1;
+      p_stage = p_stage + 1 == kStages ? 0 : p_stage + 1;
       if (--p_left > 0) {
         p_tile += kWarps;
         settle();
@@ -393,11 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
     cp_async_commit();
   };
   load_q(s, g);
-  issue();
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) issue();
   zero_empty();
 
   // ---- the run, item by item
-  int stage = 0;
+  int stage = 0, item = 0;
   bool first = true;
   const int run_tiles = (int)run;
   for (int u = 0; u < run_tiles;) {
@@ -446,13 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
     const int kend = u + piece, base = u - tile0;
     k0 += (warp + kWarps - k0 % kWarps) % kWarps;
     for (int k = k0; k < kend; k += kWarps) {
-      cp_async_wait<0>();
+      cp_async_wait<kStages - 2>();
       __syncwarp();
       issue();
       const uint8_t* st = &sm.ring[warp][stage][0];
       const int valid = n - (k - base) * kTok;
       const int2 ok = *reinterpret_cast<const int2*>(&sm.page_ok[warp][stage][0]);
-      stage ^= 1;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
       const bool edge = valid < kTok || !ok.x || !ok.y;
       // this lane's tokens: rows r and r + 8 of the first product
       const int p0 = 4 * (r >> 1) + (r & 1), p1 = p0 + 2;
@@ -553,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float to = top > m[t][b] + kSlack ? top : m[t][b];
+            float to = top > m[t][b] + kSlack ? top : m[t][b];
+            if (kTwice) to = __shfl_sync(0xffffffffu, to, lane & ~2);   // columns agree
             f[b] = to == -INFINITY ? 1.f : exp2f(m[t][b] - to);
             m[t][b] = to;
           }
@@ -677,8 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
       }
       load_q(next_s, next_g);
     }
-    const bool whole = piece == nt;
-    float* part = a.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * part_floats(G, D);
+    // Each warp leaves its sums in a slot and goes on; kJoiners of them, in
+    // turn, wait for the others' and add up.
+    const int slot = item % S::kSlots, turn = item / S::kSlots;
+    if (turn > 0 && !wait_for(&sm.free[slot], (turn - 1) & 1, a.status)) break;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float2 l = unpair(l2[t]);
@@ -688,75 +717,76 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
         l.y += __shfl_xor_sync(0xffffffffu, l.y, x);
       }
       if (r == 0 && (!kTwice || c < 2)) {
-        *reinterpret_cast<float2*>(&sm.m[warp][2 * c + 8 * t]) = make_float2(m[t][0], m[t][1]);
-        *reinterpret_cast<float2*>(&sm.l[warp][2 * c + 8 * t]) = l;
+        *reinterpret_cast<float2*>(&sm.m[slot][warp][2 * c + 8 * t]) =
+            make_float2(m[t][0], m[t][1]);
+        *reinterpret_cast<float2*>(&sm.l[slot][warp][2 * c + 8 * t]) = l;
       }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int h = 2 * (kTwice ? c & 1 : c) + b;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][h + 8 * t]);
-        const float f = m[t][b] == -INFINITY ? 0.f : exp2f(m[t][b] - M);
+        const int h = 2 * (kTwice ? c & 1 : c) + b + 8 * t;
 #pragma unroll
         for (int gr = 0; gr < NG; gr += kTwice ? 2 : 1) {
           const bool odd = kTwice && c >= 2;           // this column's group
-          const uint32_t un = (unit[gr / 2] >> (kTwice ? (odd ? 23 : 7) : 16 * (gr % 2) + 7)) & 0xffu;
-          const float v = exp2f((float)(127 - (int)un));
+          const uint32_t un =
+              (unit[gr / 2] >> (kTwice ? (odd ? 23 : 7) : 16 * (gr % 2) + 7)) & 0xffu;
+          const float v = __uint_as_float((254 - un) << 23);   // 1 / unit
           float x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             x[i] = (odd ? o[t][kTwice ? gr + 1 : gr][i / 2][2 * (i % 2) + b]
-                        : o[t][gr][i / 2][2 * (i % 2) + b]) * v * f;
-          *reinterpret_cast<float4*>(&sm.o[warp][h][32 * (gr + odd) + 4 * r]) =
+                        : o[t][gr][i / 2][2 * (i % 2) + b]) * v;
+          *reinterpret_cast<float4*>(&sm.o[slot][warp][h][32 * (gr + odd) + 4 * r]) =
               make_float4(x[0], x[1], x[2], x[3]);
         }
       }
-      __syncthreads();
-      const int heads = G - 8 * t < 8 ? G - 8 * t : 8;
-      for (int i = tid; i < heads * (D / 4); i += kThreads) {
+    }
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&sm.full[slot]);
+    if (warp / kJoiners == item % (kWarps / kJoiners)) {
+      if (!wait_for(&sm.full[slot], turn & 1, a.status)) break;
+      const bool whole = piece == nt;
+      float* part = a.part + ((size_t)me * 2 + (first ? 0 : 1)) * part_floats(G, D);
+      for (int i = (warp % kJoiners) * 32 + lane; i < G * (D / 4); i += kJoiners * 32) {
         const int h = i / (D / 4), d4 = 4 * (i % (D / 4));
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][h + 8 * t]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[slot][w][h]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = sm.m[w][h + 8 * t];
-          L += sm.l[w][h + 8 * t] * (mw == -INFINITY ? 0.f : exp2f(mw - M));
-          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][h][d4]);
-          acc.x += x.x;
-          acc.y += x.y;
-          acc.z += x.z;
-          acc.w += x.w;
+          const float mw = sm.m[slot][w][h];
+          const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[slot][w][h][d4]);
+          L = fmaf(sm.l[slot][w][h], f, L);
+          acc.x = fmaf(x.x, f, acc.x);
+          acc.y = fmaf(x.y, f, acc.y);
+          acc.z = fmaf(x.z, f, acc.z);
+          acc.w = fmaf(x.w, f, acc.w);
         }
-        const int hh = h + 8 * t;
         if (whole) {
-          const size_t row = (size_t)s * a.Hq + (size_t)g * G + hh;
+          const size_t row = (size_t)s * a.Hq + (size_t)g * G + h;
           const float inv = L == 0.f ? 0.f : 1.f / L;
           *reinterpret_cast<uint2*>(a.out + row * D + d4) =
               make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
           if (a.lse && d4 == 0)
             a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         } else {
-          *reinterpret_cast<float4*>(part + (size_t)hh * D + d4) = acc;
+          *reinterpret_cast<float4*>(part + (size_t)h * D + d4) = acc;
           if (d4 == 0) {
-            part[(size_t)G * D + hh] = M;
-            part[(size_t)G * D + G + hh] = L;
+            part[(size_t)G * D + h] = M;
+            part[(size_t)G * D + G + h] = L;
           }
         }
       }
-      __syncthreads();
+      // the first part of an item that goes on in the next CTAs
+      if (!whole && tile0 == 0 && lane == 0 && warp % kJoiners == 0) {
+        const int all = parts ? parts : cta_of(u0 + u + nt - 1, total, ctas) - me + 1;
+        a.desc[me] = Desc{s, g, all, first ? 0 : 1};
+      }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&sm.free[slot]);
     }
-    // the first part of an item that goes on in the next CTAs
-    if (!whole && tile0 == 0 && tid == 0) {
-      const int all = parts ? parts : cta_of(u0 + u + nt - 1, total, ctas) - me + 1;
-      a.desc[me] = Desc{s, g, all, first ? 0 : 1};
-    }
+    ++item;
     u += piece;
     tile0 = 0;
     first = false;
