@@ -21,6 +21,7 @@ from . import _lib
 
 
 _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+_CONTIGUOUS = torch.contiguous_format
 
 
 def _device(name, t):
@@ -49,7 +50,8 @@ def _dense(name, t, dtype, device, shape=None):
 def _rows(name, t, device, shape=None):
     """Token stride of a bf16 ``[tokens, heads, head_dim]`` tensor whose heads
     are dense."""
-    if _device(name, t) != device:
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _device(name, t)
         raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
     if t.dtype is not _BF16:
         raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
@@ -70,14 +72,17 @@ def _table(block_table, device, nseq):
     return block_table.shape[1]
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _call(name, device, *args):
     """Run a C entry on CUDA device ``device``'s current stream."""
     fn = getattr(_lib.load(), name)
-    if device == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if device == _current_device():
+        st = fn(*args, _current_stream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+            st = fn(*args, _current_stream(device))
     if st:
         _lib.check(name, st)
 
@@ -134,8 +139,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
         _dense("k_weight", k_weight, _BF16, dev, (d,))
         qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
     if out is None:
-        q_out = torch.empty(T, Hq, d, dtype=_BF16, device=dev)
-        k_out = torch.empty(T, Hkv, d, dtype=_BF16, device=dev)
+        q_out = torch.empty_like(q, memory_format=_CONTIGUOUS)
+        k_out = torch.empty_like(k, memory_format=_CONTIGUOUS)
         qo_stride, ko_stride = Hq * d, Hkv * d
     else:
         q_out, k_out = out
