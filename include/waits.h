@@ -406,7 +406,8 @@ waits_status waits_decode_attention(int32_t nseq, int32_t num_q_heads, int32_t n
  *               values: views of a fused projection's output fit); 16-byte
  *               aligned
  *   positions   DEVICE int32 [num_tokens], any values
- *   inv_freq    HOST double [rotary_dim / 2], finite; read before the call returns
+ *   inv_freq    HOST double [rotary_dim / 2], at most 1e12 in magnitude; read
+ *               before the call returns
  *   q_weight, k_weight  DEVICE bf16 [d], 16-byte aligned, or both NULL
  *   q_out, k_out  as q, k with their own strides.  An output may be its own
  *               input (same pointer and stride); any other overlap with an

@@ -69,7 +69,7 @@ waits_status waits_qk_norm_rope(int32_t num_tokens, int32_t num_q_heads, int32_t
   if (rotary_dim < 8 || rotary_dim > head_dim || rotary_dim % 8) return WAITS_ERR_SHAPE;
   if (!inv_freq || !std::isfinite(eps) || eps < 0.0f) return WAITS_ERR_ARG;
   for (int i = 0; i < rotary_dim / 2; ++i)
-    if (!std::isfinite(inv_freq[i])) return WAITS_ERR_ARG;
+    if (!(std::fabs(inv_freq[i]) <= 1e12)) return WAITS_ERR_ARG;   // NaN too
   if ((q_weight == nullptr) != (k_weight == nullptr)) return WAITS_ERR_ARG;
   if (!stride_ok(q_stride, num_q_heads, head_dim) ||
       !stride_ok(k_stride, num_kv_heads, head_dim) ||

@@ -18,81 +18,59 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kCtas = 8;
 
-// Inclusive prefix sums of two 64-bit values over the block's threads.
-__device__ inline void block_scan2(int64_t& a, int64_t& b, int64_t (*sa)[2]) {
+// Inclusive prefix sum over the block's threads; `sums` is shared memory that
+// no thread still reads (two calls in a row take two).
+__device__ inline int64_t block_scan(int64_t x, int64_t* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) {
-      a += x;
-      b += y;
-    }
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  if (lane == 31) {
-    sa[warp][0] = a;
-    sa[warp][1] = b;
-  }
+  if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int64_t x = sa[lane][0], y = sa[lane][1];
+  int64_t before = lane < warp ? sums[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) {
-        x += u;
-        y += v;
-      }
-    }
-    sa[lane][0] = x;
-    sa[lane][1] = y;
-  }
-  __syncthreads();
-  if (warp) {
-    a += sa[warp - 1][0];
-    b += sa[warp - 1][1];
-  }
-  __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  return x + before;
 }
 
 // Shared memory: cu[nseq + 1] (where the sequence's tokens start, cut to
-// 2^31 - 1), first[nseq] (its first block on the stack, -1 refused).
+// 2^31 - 1), first[nseq] (its first block on the stack, -1 refused), and its
+// length so far.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t scan[32][2];
+  __shared__ int64_t scan[2][32];
   __shared__ int64_t total[2];
   __shared__ int taken;
   int32_t* cu = sm;
   int32_t* first = sm + a.nseq + 1;
-  auto cluster = cooperative_groups::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  int32_t* held = first + a.nseq;
+  const int rank = blockIdx.x, ranks = gridDim.x;
   const int t = threadIdx.x;
   const int bs1 = (1 << a.log_bs) - 1;
   const int64_t cap = (int64_t)a.width << a.log_bs;
   uint32_t bits = 0;
-  pdl_allow_next();
-  pdl_wait();
   if (t == 0) {
     cu[0] = 0;
     total[0] = total[1] = 0;
     taken = 0;
   }
+  pdl_allow_next();
+  pdl_wait();
   int free_n = *a.free_count;
   free_n = free_n < 0 ? 0 : (free_n > a.num_blocks ? a.num_blocks : free_n);
-  __syncthreads();
   for (int s0 = 0; s0 < a.nseq; s0 += kThreads) {
     const int s = s0 + t;
-    int64_t need = 0, toks = 0;
     int len = 0, add = 0;
     if (s < a.nseq) {
       len = a.cache_len[s];
       add = a.new_len[s];
-      toks = add > 0 ? add : 0;
     }
+    __syncthreads();                     // total, and scan's readers
     // the tokens first: whether the slots fit decides what a sequence needs
-    int64_t upto = toks, dummy = 0;
-    block_scan2(upto, dummy, scan);
-    upto += total[1];
+    const int64_t upto = block_scan(add > 0 ? add : 0, scan[0]) + total[1];
     bool ok = s < a.nseq;
     if (ok && (len < 0 || add < 0)) {
       ok = false;
@@ -102,11 +80,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
       bits |= WAITS_DEV_CACHE_FULL;
     }
     const int64_t have = ((int64_t)len + bs1) >> a.log_bs;
-    if (ok) need = (((int64_t)len + add + bs1) >> a.log_bs) - have;
-    int64_t blocks = need;
-    dummy = 0;
-    block_scan2(blocks, dummy, scan);
-    blocks += total[0];
+    const int64_t need = ok ? (((int64_t)len + add + bs1) >> a.log_bs) - have : 0;
+    const int64_t blocks = block_scan(need, scan[1]) + total[0];
     if (ok && need > 0 && blocks > free_n) {
       ok = false;
       bits |= WAITS_DEV_CACHE_FULL;
@@ -114,6 +89,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
     if (s < a.nseq) {
       cu[s + 1] = (int32_t)(upto < 0x7fffffff ? upto : 0x7fffffff);
       first[s] = ok ? (int32_t)(blocks - need) : -1;
+      held[s] = len;
       if (ok && need > 0) atomicMax(&taken, (int)blocks);
     }
     __syncthreads();
@@ -121,57 +97,66 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
       total[0] = blocks;
       total[1] = upto;
     }
-    __syncthreads();
   }
-  // slots, four neighbouring tokens per thread and step
-  const int tid = rank * kThreads + t;
+  // slots, four neighbouring tokens per thread and step: their block is
+  // looked up once, or where it changes
   const int ntok = cu[a.nseq] < a.max_new ? cu[a.nseq] : a.max_new;
-  for (int64_t i0 = (int64_t)tid * 4; i0 < a.max_new; i0 += (int64_t)kCtas * kThreads * 4) {
-    int s = 0;
-    if (i0 < ntok) {                     // last s with cu[s] <= i0
-      int lo = 0, hi = a.nseq;
+  const bool vec = a.slots && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
+#pragma unroll 2
+  for (int64_t i0 = (int64_t)(rank * kThreads + t) * 4; i0 < a.max_new;
+       i0 += (int64_t)ranks * kThreads * 4) {
+    int slot[4] = {-1, -1, -1, -1};
+    if (i0 < ntok) {
+      int lo = 0, hi = a.nseq;           // the last s with cu[s] <= i0
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cu[mid] <= i0) lo = mid; else hi = mid;
       }
-      s = lo;
-    }
-    for (int e = 0; e < 4; ++e) {
-      const int64_t i = i0 + e;
-      if (i >= a.max_new) break;
-      int slot = -1;
-      if (i < ntok) {
-        while (cu[s + 1] <= i) ++s;
-        if (first[s] >= 0) {
-          const int len = a.cache_len[s];
-          const int pos = len + (int)(i - cu[s]);
+      int s = lo, block = -1;
+      bool fresh = true;                 // the block is not known yet
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = i0 + e;
+        if (i >= ntok) break;
+        while (cu[s + 1] <= i) {
+          ++s;
+          fresh = true;
+        }
+        if (first[s] < 0) continue;
+        const int len = held[s];
+        const int pos = len + (int)(i - cu[s]);
+        if (fresh || (pos & bs1) == 0) {
           const int logical = pos >> a.log_bs;
           const int have = (int)(((int64_t)len + bs1) >> a.log_bs);
           int32_t* entry = a.table + (int64_t)s * a.width + logical;
-          int block;
           if (logical < have) {
             block = *entry;
           } else {
-            block = a.free_list[free_n - 1 - (first[s] + logical - have)];
+            block = __ldg(a.free_list + (free_n - 1 - (first[s] + logical - have)));
             // the first token of a block is always a new one
             if ((pos & bs1) == 0) *entry = block;
           }
-          if ((unsigned)block < (unsigned)a.num_blocks)
-            slot = (block << a.log_bs) + (pos & bs1);
-          else
-            bits |= WAITS_DEV_BAD_INDEX;
+          fresh = false;
         }
+        if ((unsigned)block < (unsigned)a.num_blocks)
+          slot[e] = (block << a.log_bs) + (pos & bs1);
+        else
+          bits |= WAITS_DEV_BAD_INDEX;
       }
-      if (a.slots) a.slots[i] = slot;
     }
+    if (vec && i0 + 4 <= a.max_new)
+      *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    else if (a.slots)
+      for (int e = 0; e < 4 && i0 + e < a.max_new; ++e) a.slots[i0 + e] = slot[e];
   }
   if (a.status && bits) atomicOr(a.status, bits);
-  cluster.sync();                        // nobody reads the old lengths and count any more
+  if (CLUSTER)
+    cooperative_groups::this_cluster().sync();   // every CTA has read the lengths and the count
+  else
+    __syncthreads();
   if (rank != 0) return;
-  for (int s = t; s < a.nseq; s += kThreads) {
-    const int len = a.cache_len[s];
-    a.len_out[s] = first[s] >= 0 ? len + a.new_len[s] : len;
-  }
+  for (int s = t; s < a.nseq; s += kThreads)
+    a.len_out[s] = first[s] >= 0 ? held[s] + (cu[s + 1] - cu[s]) : held[s];
   if (a.cu_new)
     for (int s = t; s <= a.nseq; s += kThreads) a.cu_new[s] = cu[s];
   if (t == 0) *a.count_out = free_n - taken;
@@ -184,7 +169,7 @@ __global__ void __launch_bounds__(kThreads)
                    int32_t* len, int32_t* table, int32_t* free_list, int32_t* free_count,
                    uint32_t* status) {
   extern __shared__ int32_t base[];      // [nseq] first place on the stack
-  __shared__ int64_t scan[32][2];
+  __shared__ int64_t scan[32];
   __shared__ int64_t total;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int bs1 = (1 << log_bs) - 1;
@@ -218,8 +203,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int s0 = 0; s0 < nseq; s0 += kThreads) {
     const int s = s0 + t;
     const int64_t c = s < nseq ? base[s] : 0;
-    int64_t a = c, b = 0;
-    block_scan2(a, b, scan);
+    const int64_t a = block_scan(c, scan);
     if (s < nseq) {
       const int64_t at = total + a - c;
       base[s] = (int)(at < num_blocks ? at : num_blocks);
@@ -256,13 +240,17 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t st) {
-  const size_t smem = (2 * (size_t)a.nseq + 1) * sizeof(int32_t);
+  const size_t smem = (3 * (size_t)a.nseq + 1) * sizeof(int32_t);
+  // one CTA where it writes a few slots per thread: no cluster to gather
+  const bool one = a.max_new <= 4 * kThreads;
+  auto kernel = one ? reserve_kernel<false> : reserve_kernel<true>;
   if (smem > 40 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(
-        reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
   }
-  return launch_pdl_cluster(reserve_kernel, dim3(kCtas), dim3(kThreads), kCtas, smem, st, a);
+  return one ? launch_pdl(kernel, dim3(1), dim3(kThreads), smem, st, a)
+             : launch_pdl_cluster(kernel, dim3(kCtas), dim3(kThreads), kCtas, smem, st, a);
 }
 
 cudaError_t launch_release(int nseq, int log_bs, int width, int num_blocks, const int32_t* ended,

@@ -19,6 +19,7 @@ namespace waits {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kAhead = 4;   // steps of head rows whose loads a warp has in flight
 
 struct RopeParams {
   const uint16_t *q, *k, *qw, *kw;
@@ -26,7 +27,7 @@ struct RopeParams {
   int64_t qs, ks, qos, kos;
   const int32_t* pos;
   int T, Hq, Hkv, rot;
-  int warps_per_token, iters_per_warp;
+  int warps_per_token, rows_per_warp;
   float eps;
   uint64_t turns[64];   // inv_freq / (2 pi) mod 1, as a fraction of 2^64
 };
@@ -56,7 +57,6 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int lane = threadIdx.x & 31;
   const int64_t t = warp / p.warps_per_token;
   if (t >= p.T) return;
-  const int it0 = (int)(warp - t * p.warps_per_token) * p.iters_per_warp;
   const int l = lane % kLanes, sub = lane / kLanes;
   const bool turn = l < p.rot / 8;
   const int o1 = turn ? 4 * l : p.rot + 8 * (l - p.rot / 8);
@@ -75,58 +75,74 @@ __global__ void __launch_bounds__(kRopeThreads)
       sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);
     }
   }
-  float wq[8], wk[8];
-  if (NORM) {
-    unpack4(*reinterpret_cast<const uint2*>(p.qw + o1), wq);
-    unpack4(*reinterpret_cast<const uint2*>(p.qw + o2), wq + 4);
-    unpack4(*reinterpret_cast<const uint2*>(p.kw + o1), wk);
-    unpack4(*reinterpret_cast<const uint2*>(p.kw + o2), wk + 4);
-  }
-  const int rows = p.Hq + p.Hkv;
-  for (int it = it0; it < it0 + p.iters_per_warp && it * kRows < rows; ++it) {
-    const int row = it * kRows + sub;
-    const bool live = row < rows, isq = row < p.Hq;
-    const int h = isq ? row : row - p.Hq;
-    const uint16_t* src = (isq ? p.q + t * p.qs : p.k + t * p.ks) + (int64_t)h * D;
-    float x[8] = {};
-    if (live) {
-      unpack4(*reinterpret_cast<const uint2*>(src + o1), x);
-      unpack4(*reinterpret_cast<const uint2*>(src + o2), x + 4);
-    }
+  // Rows [r0, r1) of one tensor, kRows at once and kAhead of those in flight.
+  // An output may be its input: a warp's rows are its own, and every lane
+  // reads its values of a row before it writes them.
+  auto rows = [&](const uint16_t* src, uint16_t* dst, const uint16_t* weight, int r0, int r1) {
+    float w[8];
     if (NORM) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= r * (isq ? wq[e] : wk[e]);
+      unpack4(*reinterpret_cast<const uint2*>(weight + o1), w);
+      unpack4(*reinterpret_cast<const uint2*>(weight + o2), w + 4);
     }
-    float y[8];
+    for (int row0 = r0; row0 < r1; row0 += kRows * kAhead) {
+      uint2 v[kAhead][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int a = INTER ? 2 * e : e, b = INTER ? 2 * e + 1 : e + 4;
-      y[a] = x[a] * cs[e] - x[b] * sn[e];
-      y[b] = x[b] * cs[e] + x[a] * sn[e];
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = row0 + i * kRows + sub;
+        v[i][0] = v[i][1] = make_uint2(0, 0);
+        if (row < r1) {
+          v[i][0] = *reinterpret_cast<const uint2*>(src + (int64_t)row * D + o1);
+          v[i][1] = *reinterpret_cast<const uint2*>(src + (int64_t)row * D + o2);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = row0 + i * kRows + sub;
+        float x[8], y[8];
+        unpack4(v[i][0], x);
+        unpack4(v[i][1], x + 4);
+        if (NORM) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int a = INTER ? 2 * e : e, b = INTER ? 2 * e + 1 : e + 4;
+          y[a] = x[a] * cs[e] - x[b] * sn[e];
+          y[b] = x[b] * cs[e] + x[a] * sn[e];
+        }
+        if (row < r1) {
+          *reinterpret_cast<uint2*>(dst + (int64_t)row * D + o1) =
+              make_uint2(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]));
+          *reinterpret_cast<uint2*>(dst + (int64_t)row * D + o2) =
+              make_uint2(pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
+        }
+      }
     }
-    if (!live) continue;
-    uint16_t* dst = (isq ? p.qo + t * p.qos : p.ko + t * p.kos) + (int64_t)h * D;
-    *reinterpret_cast<uint2*>(dst + o1) = make_uint2(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]));
-    *reinterpret_cast<uint2*>(dst + o2) = make_uint2(pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
-  }
+  };
+  const int r0 = (int)(warp - t * p.warps_per_token) * p.rows_per_warp;
+  const int r1 = min(r0 + p.rows_per_warp, p.Hq + p.Hkv);
+  if (r0 < p.Hq) rows(p.q + t * p.qs, p.qo + t * p.qos, p.qw, r0, min(r1, p.Hq));
+  if (r1 > p.Hq)
+    rows(p.k + t * p.ks, p.ko + t * p.kos, p.kw, max(r0 - p.Hq, 0), r1 - p.Hq);
 }
 
 template <int D>
 cudaError_t launch_rope_d(const RopeArgs& a, RopeParams& p, cudaStream_t st) {
   constexpr int kRows = 32 / (D / 8);
-  const int iters = (a.Hq + a.Hkv + kRows - 1) / kRows;
+  const int rows = a.Hq + a.Hkv, steps = (rows + kRows - 1) / kRows;
   // one warp per token where the tokens alone fill the GPU (148 SMs x 32
   // warps); fewer head rows per warp where they do not
   int wpt = (148 * 32 + a.T - 1) / a.T;
-  wpt = wpt < 1 ? 1 : (wpt > iters ? iters : wpt);
-  p.iters_per_warp = (iters + wpt - 1) / wpt;
-  p.warps_per_token = (iters + p.iters_per_warp - 1) / p.iters_per_warp;
+  wpt = wpt < 1 ? 1 : (wpt > steps ? steps : wpt);
+  p.rows_per_warp = (steps + wpt - 1) / wpt * kRows;
+  p.warps_per_token = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
   const int64_t warps = (int64_t)a.T * p.warps_per_token;
   const int64_t blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -158,10 +174,11 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   p.rot = a.rot;
   p.eps = a.eps;
   for (int i = 0; i < a.rot / 2; ++i) {
-    long double t = (long double)a.inv_freq[i] / 6.283185307179586476925286766559005768L;
-    t -= floorl(t);
-    const long double f = t * 18446744073709551616.0L;
-    p.turns[i] = f >= 18446744073709551615.0L ? ~0ull : (uint64_t)f;
+    // inv_freq / (2 pi) with a mantissa of 64 bits; its fraction as 0.64,
+    // modulo 2^64 (a negative frequency turns the other way)
+    const long double t = (long double)a.inv_freq[i] * 0.159154943091895335768883763372514362L;
+    const long double f = (t - (long double)(int64_t)t) * 18446744073709551616.0L;
+    p.turns[i] = f < 0 ? 0 - (uint64_t)-f : (uint64_t)f;
   }
   return a.d == 64 ? launch_rope_d<64>(a, p, st) : launch_rope_d<128>(a, p, st);
 }
