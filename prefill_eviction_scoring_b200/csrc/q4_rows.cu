@@ -1,15 +1,21 @@
 // Rows of K and V into the 4-bit paged cache and back.
 //
 // A group of 32 dimensions has scale s = bf16(max|x| / 6) and codes
-// e2m1(x / s).  x has 8 significant bits, s has 8, the midpoints between
-// codes at most 3, so x / s is either a midpoint exactly or at least 2^-12 of
-// it away: the fp32 quotient rounds to the same code as the exact one.
+// e2m1(x / s), to the nearest, ties to even.  Ties have to be exact, and they
+// come out so without a division: x and s have 8 significant bits, a midpoint
+// t between codes is T / 4 with T < 8 bits: 1, 3, 5, 7 (or twice or four times
+// that), so x / s is t exactly or at least t / (255 T) >= 1/1020 from it, while
+// x * (1 / s) is off by less than 2^-20.  Rounding it to a multiple of 2^-10
+// (one fma that adds 1.5 * 2^13) therefore gives t if the quotient is t, and
+// stays on its side of t if it is not.
 //
 // HBM bounds it: 4 bytes read and 1.125 written per (K, V) pair of values.
-// A thread takes 8 dimensions of one row (16-byte loads).  The four threads
-// of a group share the maximum by shuffles, and pairs of threads trade two
-// bytes of codes so that each stores a whole word: the codes that one thread
-// makes lie in two places of the page's byte order.
+// A thread takes 16 dimensions of one row, half a group: the largest
+// magnitude costs one shuffle, and the address, the scale and its reciprocal
+// are shared by 16 values (8 dimensions per thread: 16.1 us against XX for
+// 16001 rows of 4 heads, the instructions bound it).  The codes that one
+// thread makes lie in four places of the page's byte order, two bytes each;
+// pairs of threads trade half of theirs and store whole words.
 #include "q4.cuh"
 
 namespace waits {
@@ -17,89 +23,127 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The word of a row's codes that thread t (of D / 8) stores or loads, and
-// the partner it trades with.  K: dimensions 8 t .. 8 t + 7 are the pairs of
-// bytes c * d/8 + 2 s for s = t / 2 and c = 2 (t % 2), + 1; neighbouring s
-// are neighbours in memory, so threads t and t ^ 2 trade.  V: r * d/16 + 2 g
-// for g = t / 4 and r = 2 (t % 4), + 1; threads t and t ^ 4 trade.
-template <int D>
-struct RowWord {
-  __host__ __device__ static constexpr int other(int which) { return which == 0 ? 2 : 4; }
-  __device__ static bool second(int which, int t) { return t & other(which); }
-  __device__ static int at(int which, int t) {
-    return which == 0 ? (2 * (t & 1) + (t >> 1 & 1)) * (D / 8) + 4 * (t >> 2)
-                      : (2 * (t & 3) + (t >> 2 & 1)) * (D / 16) + 4 * (t >> 3);
+// Where thread t (of D / 16) of a row keeps its two words of codes.
+// K: dimensions 16 t + 4 c .. + 3 are the two bytes at c * d/8 + 2 t, so
+// threads t and t ^ 1 trade, and t keeps c = 0, 1 or 2, 3.
+// V: dimensions 16 t + 4 j .. + 3 are the two bytes at r * d/16 + 2 g with
+// g = t / 2, r = 4 (t % 2) + j, so threads t and t ^ 2 trade, and t keeps
+// j = 0, 1 or 2, 3.
+template <int D, int WHICH>
+struct RowWords {
+  static constexpr int kOther = WHICH == 0 ? 1 : 2;
+  static constexpr int kStep = WHICH == 0 ? D / 8 : D / 16;   // from the first word to the second
+  __device__ static bool second(int t) { return t & kOther; }
+  __device__ static int at(int t) {
+    return WHICH == 0 ? 2 * (t & 1) * (D / 8) + 4 * (t >> 1)
+                      : (4 * (t & 1) + (t & 2)) * (D / 16) + 4 * (t >> 2);
   }
 };
 
-// Quantise 8 dimensions [8 t, 8 t + 8) of a row and store codes and scale.
-// All lanes of the warp take part; `live` ones store.
-template <int D, int WHICH>
-__device__ inline void store_row8(uint4 v, int t, bool live, uint8_t* page, int log_bs, int off) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  // the largest magnitude by its bits, so that a NaN counts as the largest
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
-  m = max(m & 0xffffu, m >> 16);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  uint32_t sb = pack_bf16(__fdiv_rn(__uint_as_float(m << 16), 6.f), 0.f) & 0xffffu;
-  if (sb < 0x0080u) sb = 0;              // below 2^-126: zeros
-  if (m >= 0x7f80u) sb = 0x7fffu;        // an infinity or NaN: NaN
-  const float s = __uint_as_float(sb << 16);
-  const bool zero = sb == 0 || sb == 0x7fffu;
-  // x / s with s scaled into [1, 2), by the reciprocal and one correction:
-  // the residual is exact, so a quotient that is a midpoint comes out exactly
-  const float f = __uint_as_float(zero ? 0u : 0x7f000000u - ((sb & 0x7f80u) << 16));
-  const float s1 = s * f, inv = zero ? 0.f : __frcp_rn(s1);
-  uint32_t c[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float q[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const float x = (b ? bf16_hi(w[e]) : bf16_lo(w[e])) * f, y = x * inv;
-      q[b] = fmaf(fmaf(-y, s1, x), inv, y);
-    }
-    c[e] = zero ? 0u : e2m1x2(q[0], q[1]);
-  }
-  const uint32_t mine[2] = {c[0] | (c[1] << 8), c[2] | (c[3] << 8)};
-  constexpr int kOther = RowWord<D>::other(WHICH);
-  const bool second = RowWord<D>::second(WHICH, t);
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? mine[0] : mine[1], kOther);
-  const uint32_t word = second ? got | (mine[1] << 16) : mine[0] | (got << 16);
-  if (!live) return;
-  *reinterpret_cast<uint32_t*>(page + Q4Page<D>::code(WHICH, log_bs, off) +
-                               RowWord<D>::at(WHICH, t)) = word;
-  if ((t & 3) == 0)
-    *reinterpret_cast<uint16_t*>(page + Q4Page<D>::scale(WHICH, log_bs, off) + 2 * (t >> 2)) =
-        (uint16_t)sb;
+__device__ inline float max_abs3(float a, float b, float c) {   // a NaN wins
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Eight values -> eight e2m1 codes, the first in the low nibble: to nearest,
+// ties to the even code, saturating at 6.
+__device__ inline uint32_t e2m1x8(const float* x) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
 }
 
-// 8 dimensions of a stored row, as bf16.  All lanes take part.
+// Quantise dimensions [16 t, 16 t + 16) of a row and store codes and scale
+// (`code`, `scale`: the row's).  All lanes of the warp take part; `live` ones
+// store.
 template <int D, int WHICH>
-__device__ inline uint4 load_row8(const uint8_t* page, int t, bool live, int log_bs, int off) {
-  uint32_t word = 0, sb = 0;
-  if (live) {
-    word = __ldg(reinterpret_cast<const uint32_t*>(page + Q4Page<D>::code(WHICH, log_bs, off) +
-                                                   RowWord<D>::at(WHICH, t)));
-    sb = __ldg(reinterpret_cast<const uint16_t*>(page + Q4Page<D>::scale(WHICH, log_bs, off)) +
-               (t >> 2));
-  }
-  constexpr int kOther = RowWord<D>::other(WHICH);
-  const bool second = RowWord<D>::second(WHICH, t);
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? word & 0xffffu : word >> 16, kOther);
-  const uint32_t codes = second ? got | (word & 0xffff0000u) : (word & 0xffffu) | (got << 16);
-  const float s = __uint_as_float(sb << 16);
-  uint32_t h[4], o[4];
-  e2m1_to_half(codes, h);
+__device__ inline void store_row16(const uint4 (&v)[2], int t, bool live, uint8_t* code,
+                                   uint8_t* scale) {
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  float x[16], top = 0.f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = half2_to_float2(h[e]);
-    o[e] = pack_bf16(f.x * s, f.y * s);
+  for (int e = 0; e < 8; ++e) {
+    x[2 * e] = bf16_lo(w[e]);
+    x[2 * e + 1] = bf16_hi(w[e]);
+    top = max_abs3(top, x[2 * e], x[2 * e + 1]);
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  top = max_abs3(top, __shfl_xor_sync(0xffffffffu, top, 1), 0.f);
+  // max / 6, corrected by its exact residual: a bf16 midpoint stays one
+  const float sixth = top * 0.16666667f;
+  uint32_t sb = pack_bf16(fmaf(fmaf(-6.f, sixth, top), 0.16666667f, sixth), 0.f) & 0xffffu;
+  if (sb < 0x0080u) sb = 0;                        // below 2^-126: zeros
+  if (!(top < INFINITY)) sb = 0x7fffu;             // an infinity or NaN: NaN
+  const bool zero = sb == 0 || sb == 0x7fffu;
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(sb << 16)));
+  constexpr float kGrid = 12288.f;                 // 1.5 * 2^13: sums are multiples of 2^-10
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = copysignf(fmaf(x[e], inv, kGrid) - kGrid, x[e]);
+  const uint32_t lo = zero ? 0u : e2m1x8(x), hi = zero ? 0u : e2m1x8(x + 8);
+  const bool second = RowWords<D, WHICH>::second(t);
+  const uint32_t got =
+      __shfl_xor_sync(0xffffffffu, second ? lo : hi, RowWords<D, WHICH>::kOther);
+  const uint32_t a = second ? got : lo, b = second ? hi : got;
+  if (!live) return;
+  uint32_t* at = reinterpret_cast<uint32_t*>(code + RowWords<D, WHICH>::at(t));
+  at[0] = __byte_perm(a, b, 0x5410);
+  at[RowWords<D, WHICH>::kStep / 4] = __byte_perm(a, b, 0x7632);
+  if ((t & 1) == 0) *reinterpret_cast<uint16_t*>(scale + t) = (uint16_t)sb;
+}
+
+// Dimensions [16 t, 16 t + 16) of a stored row, as bf16.  All lanes take part.
+template <int D, int WHICH>
+__device__ inline void load_row16(const uint8_t* code, const uint8_t* scale, int t, bool live,
+                                  uint4 (&v)[2]) {
+  uint32_t w0 = 0, w1 = 0, sb = 0;
+  if (live) {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(code + RowWords<D, WHICH>::at(t));
+    w0 = __ldg(at);
+    w1 = __ldg(at + RowWords<D, WHICH>::kStep / 4);
+    sb = __ldg(reinterpret_cast<const uint16_t*>(scale) + (t >> 1));
+  }
+  const bool second = RowWords<D, WHICH>::second(t);
+  const uint32_t a = __byte_perm(w0, w1, 0x5410), b = __byte_perm(w0, w1, 0x7632);
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? a : b, RowWords<D, WHICH>::kOther);
+  const float s = __uint_as_float(sb << 16);
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h[4];
+    e2m1_to_half(i == 0 ? (second ? got : a) : (second ? b : got), h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = half2_to_float2(h[e]);
+      o[4 * i + e] = pack_bf16(f.x * s, f.y * s);
+    }
+  }
+  v[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  v[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The four byte ranges of a token in its page.
+template <int D>
+struct Token {
+  size_t kc, ks, vc, vs;
+  __device__ Token(const Q4Pool& c, int block, int g, int off) {
+    const size_t page = ((size_t)block * c.Hkv + g) * Q4Page<D>::bytes(c.log_bs);
+    kc = page + Q4Page<D>::code(0, c.log_bs, off);
+    ks = page + Q4Page<D>::scale(0, c.log_bs, off);
+    vc = page + Q4Page<D>::code(1, c.log_bs, off);
+    vs = page + Q4Page<D>::scale(1, c.log_bs, off);
+  }
+};
+
+__device__ inline void load32(const uint16_t* p, uint4 (&v)[2]) {
+  v[0] = __ldg(reinterpret_cast<const uint4*>(p));
+  v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
 }
 
 // Block (rows, head): thread (row, t) takes K and V of one token and head.
@@ -108,26 +152,24 @@ __global__ void __launch_bounds__(kThreads)
     append_kernel(Q4Pool c, int n, const uint16_t* __restrict__ K, int64_t ks,
                   const uint16_t* __restrict__ V, int64_t vs, const int32_t* __restrict__ slots,
                   uint32_t* status) {
-  constexpr int kT = D / 8;
+  constexpr int kT = D / 16;
   pdl_allow_next();
   pdl_wait();
   const int t = threadIdx.x % kT, g = blockIdx.y;
   const int64_t row = (int64_t)blockIdx.x * (kThreads / kT) + threadIdx.x / kT;
-  uint4 k = make_uint4(0, 0, 0, 0), x = k;
+  uint4 k[2] = {}, v[2] = {};
   int slot = -1;
   if (row < n) {
     // a row without a slot is read and dropped: the loads need not wait
     slot = __ldg(slots + row);
-    k = __ldg(reinterpret_cast<const uint4*>(K + row * ks + (int64_t)g * D) + t);
-    x = __ldg(reinterpret_cast<const uint4*>(V + row * vs + (int64_t)g * D) + t);
+    load32(K + row * ks + g * D + 16 * t, k);
+    load32(V + row * vs + g * D + 16 * t, v);
   }
   const bool live = slot >= 0 && (slot >> c.log_bs) < c.num_blocks;
   if (slot >= 0 && !live && status && t == 0 && g == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
-  const int off = slot & ((1 << c.log_bs) - 1);
-  uint8_t* page =
-      c.pool + ((size_t)(live ? slot >> c.log_bs : 0) * c.Hkv + g) * Q4Page<D>::bytes(c.log_bs);
-  store_row8<D, 0>(k, t, live, page, c.log_bs, off);
-  store_row8<D, 1>(x, t, live, page, c.log_bs, off);
+  const Token<D> at(c, live ? slot >> c.log_bs : 0, g, slot & ((1 << c.log_bs) - 1));
+  store_row16<D, 0>(k, t, live, c.pool + at.kc, c.pool + at.ks);
+  store_row16<D, 1>(v, t, live, c.pool + at.vc, c.pool + at.vs);
 }
 
 // Block (slots j, (sequence, head) sg): thread (j, t).
@@ -137,7 +179,7 @@ __global__ void __launch_bounds__(kThreads)
                    const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
                    const int32_t* __restrict__ kept_len, int nseq, int T, int B,
                    const int32_t* __restrict__ table, int width, uint32_t* status) {
-  constexpr int kT = D / 8;
+  constexpr int kT = D / 16;
   pdl_allow_next();
   pdl_wait();
   const int t = threadIdx.x % kT;
@@ -159,16 +201,14 @@ __global__ void __launch_bounds__(kThreads)
       bad = j < kept && !live;
     }
     if (bad && status && t == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
-    uint4 k4 = make_uint4(0, 0, 0, 0), v4 = k4;
+    uint4 kv[2] = {}, vv[2] = {};
     if (live) {
-      k4 = __ldg(reinterpret_cast<const uint4*>(K + (src * c.Hkv + g) * D) + t);
-      v4 = __ldg(reinterpret_cast<const uint4*>(V + (src * c.Hkv + g) * D) + t);
+      load32(K + (src * c.Hkv + g) * D + 16 * t, kv);
+      load32(V + (src * c.Hkv + g) * D + 16 * t, vv);
     }
-    const int off = j & ((1 << c.log_bs) - 1);
-    uint8_t* page =
-        c.pool + ((size_t)(live ? block : 0) * c.Hkv + g) * Q4Page<D>::bytes(c.log_bs);
-    store_row8<D, 0>(k4, t, live, page, c.log_bs, off);
-    store_row8<D, 1>(v4, t, live, page, c.log_bs, off);
+    const Token<D> at(c, live ? block : 0, g, j & ((1 << c.log_bs) - 1));
+    store_row16<D, 0>(kv, t, live, c.pool + at.kc, c.pool + at.ks);
+    store_row16<D, 1>(vv, t, live, c.pool + at.vc, c.pool + at.vs);
   }
 }
 
@@ -176,7 +216,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
     read_kernel(Q4Pool c, int n, const int32_t* __restrict__ slots, uint4* __restrict__ K,
                 uint4* __restrict__ V, uint32_t* status) {
-  constexpr int kT = D / 8;
+  constexpr int kT = D / 16;
   pdl_allow_next();
   pdl_wait();
   const int t = threadIdx.x % kT, g = blockIdx.y;
@@ -184,18 +224,20 @@ __global__ void __launch_bounds__(kThreads)
   const int slot = row < n ? __ldg(slots + row) : -1;
   const bool live = slot >= 0 && (slot >> c.log_bs) < c.num_blocks;
   if (slot >= 0 && !live && status && t == 0 && g == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
-  const uint8_t* page =
-      c.pool + ((size_t)(live ? slot >> c.log_bs : 0) * c.Hkv + g) * Q4Page<D>::bytes(c.log_bs);
-  const int off = slot & ((1 << c.log_bs) - 1);
-  const uint4 k = load_row8<D, 0>(page, t, live, c.log_bs, off);
-  const uint4 v = load_row8<D, 1>(page, t, live, c.log_bs, off);
+  const Token<D> at(c, live ? slot >> c.log_bs : 0, g, slot & ((1 << c.log_bs) - 1));
+  uint4 k[2], v[2];
+  load_row16<D, 0>(c.pool + at.kc, c.pool + at.ks, t, live, k);
+  load_row16<D, 1>(c.pool + at.vc, c.pool + at.vs, t, live, v);
   if (row >= n) return;
-  K[(row * c.Hkv + g) * kT + t] = k;
-  V[(row * c.Hkv + g) * kT + t] = v;
+  const int64_t o = ((row * c.Hkv + g) * kT + t) * 2;
+  K[o] = k[0];
+  K[o + 1] = k[1];
+  V[o] = v[0];
+  V[o + 1] = v[1];
 }
 
 unsigned blocks_for(int64_t rows, int d) {
-  return (unsigned)((rows + kThreads / (d / 8) - 1) / (kThreads / (d / 8)));
+  return (unsigned)((rows + kThreads / (d / 16) - 1) / (kThreads / (d / 16)));
 }
 
 }  // namespace
