@@ -45,6 +45,11 @@ __device__ inline float max_abs3(float a, float b, float c) {   // a NaN wins
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ inline uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 // Eight values -> eight e2m1 codes, the first in the low nibble: to nearest,
 // ties to the even code, saturating at 6.
 __device__ inline uint32_t e2m1x8(const float* x) {
@@ -84,8 +89,19 @@ __device__ inline void store_row16(const uint4 (&v)[2], int t, bool live, uint8_
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(__uint_as_float(sb << 16)));
   constexpr float kGrid = 12288.f;                 // 1.5 * 2^13: sums are multiples of 2^-10
+  const uint64_t inv2 = pack2(inv, inv), up = pack2(kGrid, kGrid), down = pack2(-kGrid, -kGrid);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = copysignf(fmaf(x[e], inv, kGrid) - kGrid, x[e]);
+  for (int e = 0; e < 16; e += 2) {
+    float q0, q1;
+    asm("{\n\t.reg .b64 y;\n\t"
+        "fma.rn.f32x2 y, %2, %3, %4;\n\t"
+        "add.rn.f32x2 y, y, %5;\n\t"
+        "mov.b64 {%0, %1}, y;\n\t}"
+        : "=f"(q0), "=f"(q1)
+        : "l"(pack2(x[e], x[e + 1])), "l"(inv2), "l"(up), "l"(down));
+    x[e] = copysignf(q0, x[e]);
+    x[e + 1] = copysignf(q1, x[e + 1]);
+  }
   const uint32_t lo = zero ? 0u : e2m1x8(x), hi = zero ? 0u : e2m1x8(x + 8);
   const bool second = RowWords<D, WHICH>::second(t);
   const uint32_t got =
@@ -98,35 +114,40 @@ __device__ inline void store_row16(const uint4 (&v)[2], int t, bool live, uint8_
   if ((t & 1) == 0) *reinterpret_cast<uint16_t*>(scale + t) = (uint16_t)sb;
 }
 
-// Dimensions [16 t, 16 t + 16) of a stored row, as bf16.  All lanes take part.
+// Dimensions [16 t, 16 t + 16) of a stored row: its words, then its values as
+// bf16.  All lanes take part in both.
 template <int D, int WHICH>
-__device__ inline void load_row16(const uint8_t* code, const uint8_t* scale, int t, bool live,
-                                  uint4 (&v)[2]) {
-  uint32_t w0 = 0, w1 = 0, sb = 0;
-  if (live) {
+struct RowWords16 {
+  uint32_t w0, w1, sb;
+  __device__ void load(const uint8_t* code, const uint8_t* scale, int t, bool live) {
+    w0 = w1 = sb = 0;
+    if (!live) return;
     const uint32_t* at = reinterpret_cast<const uint32_t*>(code + RowWords<D, WHICH>::at(t));
     w0 = __ldg(at);
     w1 = __ldg(at + RowWords<D, WHICH>::kStep / 4);
     sb = __ldg(reinterpret_cast<const uint16_t*>(scale) + (t >> 1));
   }
-  const bool second = RowWords<D, WHICH>::second(t);
-  const uint32_t a = __byte_perm(w0, w1, 0x5410), b = __byte_perm(w0, w1, 0x7632);
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? a : b, RowWords<D, WHICH>::kOther);
-  const float s = __uint_as_float(sb << 16);
-  uint32_t o[8];
+  __device__ void values(int t, uint4 (&v)[2]) const {
+    const bool second = RowWords<D, WHICH>::second(t);
+    const uint32_t a = __byte_perm(w0, w1, 0x5410), b = __byte_perm(w0, w1, 0x7632);
+    const uint32_t got =
+        __shfl_xor_sync(0xffffffffu, second ? a : b, RowWords<D, WHICH>::kOther);
+    const float s = __uint_as_float(sb << 16);
+    uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t h[4];
-    e2m1_to_half(i == 0 ? (second ? got : a) : (second ? b : got), h);
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[4];
+      e2m1_to_half(i == 0 ? (second ? got : a) : (second ? b : got), h);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = half2_to_float2(h[e]);
-      o[4 * i + e] = pack_bf16(f.x * s, f.y * s);
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = half2_to_float2(h[e]);
+        o[4 * i + e] = pack_bf16(f.x * s, f.y * s);
+      }
     }
+    v[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    v[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
-  v[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  v[1] = make_uint4(o[4], o[5], o[6], o[7]);
-}
+};
 
 // The four byte ranges of a token in its page.
 template <int D>
@@ -141,9 +162,33 @@ struct Token {
   }
 };
 
-__device__ inline void load32(const uint16_t* p, uint4 (&v)[2]) {
-  v[0] = __ldg(reinterpret_cast<const uint4*>(p));
-  v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+// 32 bytes, as one access where they are aligned to that (`wide`, the same for
+// a whole call): two 16-byte ones touch every sector twice.
+__device__ inline void load32(const uint16_t* p, bool wide, uint4 (&v)[2]) {
+  if (wide) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+          "=r"(v[1].z), "=r"(v[1].w)
+        : "l"(p));
+  } else {
+    v[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+}
+__device__ inline void store32(uint16_t* p, bool wide, const uint4 (&v)[2]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0].x),
+                 "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+                 "r"(v[1].w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = v[0];
+    reinterpret_cast<uint4*>(p)[1] = v[1];
+  }
+}
+// Whether rows at `p` with this stride (elements) are 32-byte aligned.
+bool wide_rows(const void* p, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(p) % 32 == 0 && stride % 16 == 0;
 }
 
 // Block (rows, head): thread (row, t) takes K and V of one token and head.
@@ -151,7 +196,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
     append_kernel(Q4Pool c, int n, const uint16_t* __restrict__ K, int64_t ks,
                   const uint16_t* __restrict__ V, int64_t vs, const int32_t* __restrict__ slots,
-                  uint32_t* status) {
+                  bool wide, uint32_t* status) {
   constexpr int kT = D / 16;
   pdl_allow_next();
   pdl_wait();
@@ -162,8 +207,8 @@ __global__ void __launch_bounds__(kThreads)
   if (row < n) {
     // a row without a slot is read and dropped: the loads need not wait
     slot = __ldg(slots + row);
-    load32(K + row * ks + g * D + 16 * t, k);
-    load32(V + row * vs + g * D + 16 * t, v);
+    load32(K + row * ks + g * D + 16 * t, wide, k);
+    load32(V + row * vs + g * D + 16 * t, wide, v);
   }
   const bool live = slot >= 0 && (slot >> c.log_bs) < c.num_blocks;
   if (slot >= 0 && !live && status && t == 0 && g == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
@@ -178,7 +223,7 @@ __global__ void __launch_bounds__(kThreads)
     compact_kernel(Q4Pool c, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
                    const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
                    const int32_t* __restrict__ kept_len, int nseq, int T, int B,
-                   const int32_t* __restrict__ table, int width, uint32_t* status) {
+                   const int32_t* __restrict__ table, int width, bool wide, uint32_t* status) {
   constexpr int kT = D / 16;
   pdl_allow_next();
   pdl_wait();
@@ -203,8 +248,8 @@ __global__ void __launch_bounds__(kThreads)
     if (bad && status && t == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
     uint4 kv[2] = {}, vv[2] = {};
     if (live) {
-      load32(K + (src * c.Hkv + g) * D + 16 * t, kv);
-      load32(V + (src * c.Hkv + g) * D + 16 * t, vv);
+      load32(K + (src * c.Hkv + g) * D + 16 * t, wide, kv);
+      load32(V + (src * c.Hkv + g) * D + 16 * t, wide, vv);
     }
     const Token<D> at(c, live ? block : 0, g, j & ((1 << c.log_bs) - 1));
     store_row16<D, 0>(kv, t, live, c.pool + at.kc, c.pool + at.ks);
@@ -212,31 +257,49 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <int D>
+// ROWS: rows a thread reads back at once, 2 where there are blocks enough.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
-    read_kernel(Q4Pool c, int n, const int32_t* __restrict__ slots, uint4* __restrict__ K,
-                uint4* __restrict__ V, uint32_t* status) {
+    read_kernel(Q4Pool c, int n, const int32_t* __restrict__ slots, uint16_t* __restrict__ K,
+                uint16_t* __restrict__ V, bool wide, uint32_t* status) {
   constexpr int kT = D / 16;
   pdl_allow_next();
   pdl_wait();
   const int t = threadIdx.x % kT, g = blockIdx.y;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / kT) + threadIdx.x / kT;
-  const int slot = row < n ? __ldg(slots + row) : -1;
-  const bool live = slot >= 0 && (slot >> c.log_bs) < c.num_blocks;
-  if (slot >= 0 && !live && status && t == 0 && g == 0) atomicOr(status, WAITS_DEV_BAD_INDEX);
-  const Token<D> at(c, live ? slot >> c.log_bs : 0, g, slot & ((1 << c.log_bs) - 1));
-  uint4 k[2], v[2];
-  load_row16<D, 0>(c.pool + at.kc, c.pool + at.ks, t, live, k);
-  load_row16<D, 1>(c.pool + at.vc, c.pool + at.vs, t, live, v);
-  if (row >= n) return;
-  const int64_t o = ((row * c.Hkv + g) * kT + t) * 2;
-  K[o] = k[0];
-  K[o + 1] = k[1];
-  V[o] = v[0];
-  V[o + 1] = v[1];
+  const int64_t row0 = (int64_t)blockIdx.x * (ROWS * kThreads / kT) + threadIdx.x / kT;
+  int slot[ROWS];
+  bool live[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t row = row0 + i * (kThreads / kT);
+    slot[i] = row < n ? __ldg(slots + row) : -1;
+    live[i] = slot[i] >= 0 && (slot[i] >> c.log_bs) < c.num_blocks;
+    if (slot[i] >= 0 && !live[i] && status && t == 0 && g == 0)
+      atomicOr(status, WAITS_DEV_BAD_INDEX);
+  }
+  RowWords16<D, 0> k[ROWS];
+  RowWords16<D, 1> v[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const Token<D> at(c, live[i] ? slot[i] >> c.log_bs : 0, g, slot[i] & ((1 << c.log_bs) - 1));
+    k[i].load(c.pool + at.kc, c.pool + at.ks, t, live[i]);
+    v[i].load(c.pool + at.vc, c.pool + at.vs, t, live[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t row = row0 + i * (kThreads / kT);
+    uint4 x[2], y[2];
+    k[i].values(t, x);
+    v[i].values(t, y);
+    if (row >= n) continue;
+    const int64_t o = (row * c.Hkv + g) * D + 16 * t;
+    store32(K + o, wide, x);
+    store32(V + o, wide, y);
+  }
 }
 
-unsigned blocks_for(int64_t rows, int d) {
+unsigned blocks_for(int64_t rows, int d, int per = 1) {
+  rows = (rows + per - 1) / per;
   return (unsigned)((rows + kThreads / (d / 16) - 1) / (kThreads / (d / 16)));
 }
 
@@ -247,14 +310,17 @@ cudaError_t launch_q4_append(const Q4Pool& c, int n, const uint16_t* K, int64_t 
                              uint32_t* status, cudaStream_t st) {
   auto kernel = c.d == 64 ? append_kernel<64> : append_kernel<128>;
   return launch_pdl(kernel, dim3(blocks_for(n, c.d), c.Hkv), dim3(kThreads), 0, st, c, n, K, ks,
-                    V, vs, slots, status);
+                    V, vs, slots, wide_rows(K, ks) && wide_rows(V, vs), status);
 }
 
 cudaError_t launch_q4_read(const Q4Pool& c, int n, const int32_t* slots, uint16_t* K, uint16_t* V,
                            uint32_t* status, cudaStream_t st) {
-  auto kernel = c.d == 64 ? read_kernel<64> : read_kernel<128>;
-  return launch_pdl(kernel, dim3(blocks_for(n, c.d), c.Hkv), dim3(kThreads), 0, st, c, n, slots,
-                    reinterpret_cast<uint4*>(K), reinterpret_cast<uint4*>(V), status);
+  // two rows per thread once one row's blocks would fill the SMs (8 each)
+  const int per = (int64_t)blocks_for(n, c.d) * c.Hkv > 148 * 8 ? 2 : 1;
+  auto kernel = c.d == 64 ? (per == 2 ? read_kernel<64, 2> : read_kernel<64, 1>)
+                          : (per == 2 ? read_kernel<128, 2> : read_kernel<128, 1>);
+  return launch_pdl(kernel, dim3(blocks_for(n, c.d, per), c.Hkv), dim3(kThreads), 0, st, c, n,
+                    slots, K, V, wide_rows(K, 0) && wide_rows(V, 0), status);
 }
 
 cudaError_t launch_q4_compact(const Q4Pool& c, const uint16_t* K, const uint16_t* V,
@@ -265,7 +331,7 @@ cudaError_t launch_q4_compact(const Q4Pool& c, const uint16_t* K, const uint16_t
   auto kernel = c.d == 64 ? compact_kernel<64> : compact_kernel<128>;
   return launch_pdl(kernel, dim3(blocks_for(B, c.d), (unsigned)(pairs < 65535 ? pairs : 65535)),
                     dim3(kThreads), 0, st, c, K, V, cu, idx, kept_len, nseq, T, B, table, width,
-                    status);
+                    wide_rows(K, 0) && wide_rows(V, 0), status);
 }
 
 }  // namespace waits
