@@ -166,6 +166,33 @@ __host__ __device__ inline size_t part_floats(int G, int D) {
   return ((size_t)G * (D + 2) + 3) / 4 * 4;
 }
 
+// A lane's dimensions in the join.
+template <int E>
+struct Floats;
+template <>
+struct Floats<2> {
+  using Type = float2;
+  __device__ static void scale(Type& a, float f) { a.x *= f, a.y *= f; }
+  __device__ static void add(Type& a, const Type& x, float f) {
+    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
+  }
+  __device__ static void store(uint16_t* p, const Type& a) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(a.x, a.y);
+  }
+};
+template <>
+struct Floats<4> {
+  using Type = float4;
+  __device__ static void scale(Type& a, float f) { a.x *= f, a.y *= f, a.z *= f, a.w *= f; }
+  __device__ static void add(Type& a, const Type& x, float f) {
+    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
+    a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+  }
+  __device__ static void store(uint16_t* p, const Type& a) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+  }
+};
+
 // Where part i of n of `total` tiles begins.
 __device__ inline int64_t split(int64_t total, int i, int n) {
   if (total < 1 << 22) return (uint32_t)total * (uint32_t)i / (uint32_t)n;
@@ -799,10 +826,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
 
 // Joins the parts of an item: a CTA per CTA of the first kernel, a warp per
 // head.  A lane takes the maximum and sum of every 32nd part, then the warp
-// adds up the weighted sums in order, a lane D / 32 dimensions.
+// adds up the weighted sums in order, a lane D / 32 dimensions.  Latency
+// bounds it (a few KB): all loads of up to kAtOnce parts go out together.
 template <int D>
 __global__ void __launch_bounds__(512) q4_join_kernel(const DecodeArgs a) {
-  constexpr int kE = D / 32;
+  constexpr int kE = D / 32, kAtOnce = 16;
+  using Vec = typename Floats<kE>::Type;
   pdl_allow_next();
   pdl_wait();
   const int h = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.G;
@@ -813,50 +842,44 @@ __global__ void __launch_bounds__(512) q4_join_kernel(const DecodeArgs a) {
   auto at = [&](int i) {
     return a.part + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? de.slot : 0)) * stride;
   };
-  float M = -INFINITY, L = 0.f, acc[kE] = {};
+  float M = -INFINITY, L = 0.f;
+  Vec acc = {};
   for (int i0 = 0; i0 < de.parts; i0 += 32) {
-    const int n = de.parts - i0 < 32 ? de.parts - i0 : 32;
+    const int n = min(de.parts - i0, 32);
     float m = -INFINITY, l = 0.f;
     if (lane < n) {
-      m = at(i0 + lane)[(size_t)G * D + h];
-      l = at(i0 + lane)[(size_t)G * D + G + h];
+      m = __ldg(at(i0 + lane) + (size_t)G * D + h);
+      l = __ldg(at(i0 + lane) + (size_t)G * D + G + h);
     }
-    float top = m;
+    float f = 0.f;
+    for (int j0 = 0; j0 < n; j0 += kAtOnce) {
+      Vec x[kAtOnce];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = fmaxf(top, M);
-    const float back = M == -INFINITY ? 0.f : exp2f(M - top);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - top);
-    M = top;
-    l *= f;
+      for (int j = 0; j < kAtOnce; ++j)
+        if (j0 + j < n)
+          x[j] = __ldg(reinterpret_cast<const Vec*>(at(i0 + j0 + j) + (size_t)h * D) + lane);
+      if (j0 == 0) {
+        float top = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    L = L * back + l;
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, M);
+        const float back = M == -INFINITY ? 0.f : exp2f(M - top);
+        f = m == -INFINITY ? 0.f : exp2f(m - top);
+        M = top;
+        l *= f;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] *= back;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float w = __shfl_sync(0xffffffffu, f, i);
-      const float* x = at(i0 + i) + (size_t)h * D + kE * lane;
-      if (kE == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(x);
-        acc[0] = fmaf(y.x, w, acc[0]);
-        acc[1] = fmaf(y.y, w, acc[1]);
-        acc[kE - 2] = fmaf(y.z, w, acc[kE - 2]);
-        acc[kE - 1] = fmaf(y.w, w, acc[kE - 1]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(x);
-        acc[0] = fmaf(y.x, w, acc[0]);
-        acc[1] = fmaf(y.y, w, acc[1]);
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        L = L * back + l;
+        Floats<kE>::scale(acc, back);
       }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (j0 + j < n) Floats<kE>::add(acc, x[j], __shfl_sync(0xffffffffu, f, j0 + j));
     }
   }
   const size_t row = (size_t)de.s * a.Hq + (size_t)de.g * G + h;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-  for (int e = 0; e < kE; e += 2)
-    *reinterpret_cast<uint32_t*>(a.out + row * D + kE * lane + e) =
-        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  Floats<kE>::scale(acc, L == 0.f ? 0.f : 1.f / L);
+  Floats<kE>::store(a.out + row * D + kE * lane, acc);
   if (a.lse && lane == 0)
     a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
