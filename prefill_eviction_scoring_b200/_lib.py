@@ -129,6 +129,26 @@ def load(path: str = LIB_PATH):
     return lib
 
 
+_bound = None
+
+
+def binding():
+    """The compiled binding of the cache operators (once); it brings
+    libwaits.so with it.  Never falls back to anything either."""
+    global _bound
+    if _bound is None:
+        load()
+        import torch  # noqa: F401  (its libraries, which the binding links to)
+        try:
+            from . import _binding
+        except ImportError as exc:
+            raise WaitsLibraryError(
+                f"cannot load the binding beside {LIB_PATH} (build it with `python -m "
+                f"prefill_eviction_scoring_b200.build`): {exc}") from exc
+        _bound = _binding
+    return _bound
+
+
 def check(fn: str, status: int):
     if status != WAITS_OK:
         lib = load()

@@ -39,7 +39,7 @@ constexpr int kSub = 16;              // tokens of one mma step; a page is a mul
 constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
 constexpr int kMinTiles = 8;          // tiles per CTA, where there are few
-constexpr int kEndTiles = 20;         // the end of an item inside a run, in tiles of a CTA
+constexpr int kEndTiles = 60;         // what the end of an item inside a run may cost, in tiles
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
 

@@ -1,0 +1,390 @@
+// Python binding of the operators around the 4-bit paged cache: argument
+// checks, output tensors, the current stream, and the call of libwaits.so.
+//
+// A decode step makes a handful of these calls per layer, on inputs of a few
+// hundred KB, so the host's share of a call is what counts: through ctypes
+// the checks, allocations and marshalling took 9 us of a 14 us call, against
+// 3 us for the launch itself.  The functions here take positional arguments
+// only; cache.py holds the signatures, defaults and documentation.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdarg>
+#include <cstdio>
+
+#include "waits.h"
+
+namespace {
+
+struct PythonError {};   // a Python exception is set
+
+[[noreturn]] void refuse(const char* fmt, ...) {
+  char text[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(text, sizeof(text), fmt, ap);
+  va_end(ap);
+  PyErr_SetString(PyExc_ValueError, text);
+  throw PythonError{};
+}
+
+const char* dtype_name(at::ScalarType t) {
+  switch (t) {
+    case at::kBFloat16: return "torch.bfloat16";
+    case at::kInt: return "torch.int32";
+    case at::kByte: return "torch.uint8";
+    case at::kDouble: return "torch.float64";
+    default: return c10::toString(t);
+  }
+}
+
+const at::Tensor& tensor(const char* name, PyObject* o) {
+  if (!THPVariable_Check(o)) refuse("%s must be a CUDA tensor", name);
+  return THPVariable_Unpack(o);
+}
+
+// A tensor of `type` on CUDA device `dev` (-1: any, which is then set).
+const at::Tensor& on_device(const char* name, PyObject* o, at::ScalarType type, int& dev) {
+  const at::Tensor& t = tensor(name, o);
+  if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
+  const int at = t.get_device();
+  if (dev < 0) dev = at;
+  if (at != dev) refuse("%s is on cuda:%d, not on cuda:%d", name, at, dev);
+  if (t.scalar_type() != type)
+    refuse("%s must be %s, got %s", name, dtype_name(type), dtype_name(t.scalar_type()));
+  return t;
+}
+
+const at::Tensor& dense(const char* name, PyObject* o, at::ScalarType type, int& dev) {
+  const at::Tensor& t = on_device(name, o, type, dev);
+  if (!t.is_contiguous()) refuse("%s must be contiguous", name);
+  return t;
+}
+
+// A dense vector of n values.
+const at::Tensor& vector(const char* name, PyObject* o, at::ScalarType type, int& dev, int64_t n) {
+  const at::Tensor& t = dense(name, o, type, dev);
+  if (t.dim() != 1 || t.size(0) != n)
+    refuse("%s must be one-dimensional, with %lld values", name, (long long)n);
+  return t;
+}
+
+const at::Tensor& one_value(const char* name, PyObject* o, int& dev) {
+  const at::Tensor& t = dense(name, o, at::kInt, dev);
+  if (t.numel() != 1) refuse("%s must hold one int32", name);
+  return t;
+}
+
+// bf16 [tokens, heads, head_dim] whose heads are dense; its token stride.
+const at::Tensor& rows(const char* name, PyObject* o, int& dev, int64_t& stride) {
+  const at::Tensor& t = on_device(name, o, at::kBFloat16, dev);
+  if (t.dim() != 3) refuse("%s must be [tokens, heads, head_dim]", name);
+  const int64_t T = t.size(0), H = t.size(1), d = t.size(2);
+  if ((t.stride(2) != 1 && d > 1) || (t.stride(1) != d && H > 1))
+    refuse("%s: a token's heads must be contiguous", name);
+  stride = T > 1 ? t.stride(0) : H * d;
+  return t;
+}
+
+const at::Tensor& table(PyObject* o, int& dev, int64_t nseq) {
+  const at::Tensor& t = dense("block_table", o, at::kInt, dev);
+  if (t.dim() != 2 || t.size(0) != nseq)
+    refuse("block_table must be [%lld, max_blocks]", (long long)nseq);
+  return t;
+}
+
+int32_t count(const char* name, int64_t n) {
+  if (n < 0 || n > 0x7fffffffLL) refuse("%s is out of range: %lld", name, (long long)n);
+  return (int32_t)n;
+}
+
+waits_q4_cache cache(PyObject* o, int& dev, int64_t head_dim) {
+  const at::Tensor& p = dense("pool", o, at::kByte, dev);
+  if (p.dim() != 3) refuse("pool must be uint8 [num_blocks, Hkv, page_bytes]");
+  const int64_t page = p.size(2), bs = head_dim > 0 ? page * 8 / (9 * head_dim) : 0;
+  if (bs * head_dim * 9 != page * 8)
+    refuse("a page of %lld bytes is no whole number of tokens of head_dim %lld", (long long)page,
+           (long long)head_dim);
+  return waits_q4_cache{count("num_blocks", p.size(0)), count("block_size", bs),
+                        count("Hkv", p.size(1)), count("head_dim", head_dim), p.data_ptr()};
+}
+
+uint32_t* status_word(PyObject* o, int& dev) {
+  return o == Py_None ? nullptr : static_cast<uint32_t*>(one_value("status", o, dev).data_ptr());
+}
+
+int64_t integer(const char* name, PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PythonError{};
+  (void)name;
+  return v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PythonError{};
+  return v != 0;
+}
+
+at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
+  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
+}
+
+int32_t* ints(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+
+// Makes `dev` current for the call; its current stream.
+struct Launch {
+  c10::cuda::OptionalCUDAGuard guard;
+  void* stream;
+  explicit Launch(int dev) {
+    if (dev != c10::cuda::current_device()) guard.set_index(dev);
+    stream = c10::cuda::getCurrentCUDAStream(dev).stream();
+  }
+};
+
+void check(const char* fn, waits_status st) {
+  if (st == WAITS_OK) return;
+  PyObject* m = PyImport_ImportModule("prefill_eviction_scoring_b200._lib");
+  if (m) {
+    PyObject* r = PyObject_CallMethod(m, "check", "si", fn, (int)st);
+    Py_XDECREF(r);
+    Py_DECREF(m);
+  }
+  if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s failed (%d)", fn, (int)st);
+  throw PythonError{};
+}
+
+PyObject* tuple(std::initializer_list<at::Tensor> ts) {
+  PyObject* t = PyTuple_New((Py_ssize_t)ts.size());
+  if (!t) throw PythonError{};
+  Py_ssize_t i = 0;
+  for (const at::Tensor& x : ts) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(x));
+  return t;
+}
+
+// Every entry point: the argument count, and no C++ exception into Python.
+template <PyObject* (*F)(PyObject* const*), int N>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const PythonError&) {
+    return nullptr;
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    return nullptr;
+  }
+}
+
+// q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, out
+PyObject* qk_norm_rope(PyObject* const* a) {
+  int dev = -1;
+  int64_t qs, ks, qos, kos;
+  const at::Tensor& q = rows("q", a[0], dev, qs);
+  const at::Tensor& k = rows("k", a[1], dev, ks);
+  const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), Hkv = k.size(1);
+  if (k.size(0) != T || k.size(2) != d) refuse("k must be [T, Hkv, d] like q's [T, Hq, d]");
+  const at::Tensor& pos = vector("positions", a[2], at::kInt, dev, T);
+  const at::Tensor& inv = tensor("inv_freq", a[3]);
+  if (inv.scalar_type() != at::kDouble || !inv.is_cpu() || inv.dim() != 1 || !inv.is_contiguous())
+    refuse("inv_freq must be a contiguous 1-D float64 CPU tensor");
+  const void *qw = nullptr, *kw = nullptr;
+  if (a[4] != Py_None || a[5] != Py_None) {
+    if (a[4] == Py_None || a[5] == Py_None) refuse("q_weight and k_weight come together");
+    qw = vector("q_weight", a[4], at::kBFloat16, dev, d).data_ptr();
+    kw = vector("k_weight", a[5], at::kBFloat16, dev, d).data_ptr();
+  }
+  const double eps = PyFloat_AsDouble(a[6]);
+  if (eps == -1.0 && PyErr_Occurred()) throw PythonError{};
+  const bool interleaved = truth(a[7]);
+  at::Tensor qo, ko;
+  if (a[8] == Py_None) {
+    qo = empty({T, Hq, d}, at::kBFloat16, dev);
+    ko = empty({T, Hkv, d}, at::kBFloat16, dev);
+    qos = Hq * d;
+    kos = Hkv * d;
+  } else {
+    if (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 2) refuse("out must be (q_out, k_out)");
+    qo = rows("out[0]", PyTuple_GET_ITEM(a[8], 0), dev, qos);
+    ko = rows("out[1]", PyTuple_GET_ITEM(a[8], 1), dev, kos);
+    if (qo.sizes() != q.sizes() || ko.sizes() != k.sizes())
+      refuse("out must have the shapes of q and k");
+  }
+  const Launch l(dev);
+  check("waits_qk_norm_rope",
+        waits_qk_norm_rope(count("tokens", T), count("heads", Hq), count("heads", Hkv),
+                           count("head_dim", d), count("rotary_dim", 2 * inv.numel()),
+                           interleaved, q.data_ptr(), qs, k.data_ptr(), ks, ints(pos),
+                           static_cast<const double*>(inv.data_ptr()), qw, kw, (float)eps,
+                           qo.data_ptr(), qos, ko.data_ptr(), kos, l.stream));
+  return tuple({qo, ko});
+}
+
+// new_len, cache_len, block_table, free_list, free_count, block_size, max_new,
+// in_place, status
+PyObject* cache_reserve(PyObject* const* a) {
+  int dev = -1;
+  const at::Tensor& len = dense("cache_len", a[1], at::kInt, dev);
+  const int64_t nseq = len.numel();
+  vector("cache_len", a[1], at::kInt, dev, nseq);
+  const at::Tensor& add = vector("new_len", a[0], at::kInt, dev, nseq);
+  const at::Tensor& tab = table(a[2], dev, nseq);
+  const at::Tensor& list = dense("free_list", a[3], at::kInt, dev);
+  const at::Tensor& free_n = one_value("free_count", a[4], dev);
+  const int32_t bs = count("block_size", integer("block_size", a[5]));
+  const int32_t max_new = count("max_new", integer("max_new", a[6]));
+  const bool in_place = truth(a[7]);
+  uint32_t* status = status_word(a[8], dev);
+  const at::Tensor slots = empty({max_new}, at::kInt, dev), cu = empty({nseq + 1}, at::kInt, dev);
+  const at::Tensor len_out = in_place ? len : empty({nseq}, at::kInt, dev);
+  const at::Tensor n_out = in_place ? free_n : empty(free_n.sizes(), at::kInt, dev);
+  const Launch l(dev);
+  check("waits_cache_reserve",
+        waits_cache_reserve(count("sequences", nseq), bs, count("max_blocks", tab.size(1)),
+                            count("num_blocks", list.numel()), max_new, ints(add), ints(len),
+                            ints(tab), ints(list), ints(free_n), ints(len_out), ints(n_out),
+                            max_new ? ints(slots) : nullptr, ints(cu), status, l.stream));
+  return tuple({slots, cu, len_out, n_out});
+}
+
+// ended, cache_len, block_table, free_list, free_count, block_size, status
+PyObject* cache_release(PyObject* const* a) {
+  int dev = -1;
+  const at::Tensor& len = dense("cache_len", a[1], at::kInt, dev);
+  const int64_t nseq = len.numel();
+  vector("cache_len", a[1], at::kInt, dev, nseq);
+  const at::Tensor& ended = vector("ended", a[0], at::kInt, dev, nseq);
+  const at::Tensor& tab = table(a[2], dev, nseq);
+  const at::Tensor& list = dense("free_list", a[3], at::kInt, dev);
+  const at::Tensor& free_n = one_value("free_count", a[4], dev);
+  const int32_t bs = count("block_size", integer("block_size", a[5]));
+  uint32_t* status = status_word(a[6], dev);
+  const Launch l(dev);
+  check("waits_cache_release",
+        waits_cache_release(count("sequences", nseq), bs, count("max_blocks", tab.size(1)),
+                            count("num_blocks", list.numel()), ints(ended), ints(len), ints(tab),
+                            ints(list), ints(free_n), status, l.stream));
+  Py_RETURN_NONE;
+}
+
+// K, V, slot_map, pool, status
+PyObject* q4_append(PyObject* const* a) {
+  int dev = -1;
+  int64_t ks, vs;
+  const at::Tensor& K = rows("K", a[0], dev, ks);
+  const at::Tensor& V = rows("V", a[1], dev, vs);
+  if (V.sizes() != K.sizes()) refuse("V must have K's shape");
+  const waits_q4_cache c = cache(a[3], dev, K.size(2));
+  if (c.num_kv_heads != K.size(1)) refuse("pool must have K's heads");
+  const at::Tensor& slots = vector("slot_map", a[2], at::kInt, dev, K.size(0));
+  uint32_t* status = status_word(a[4], dev);
+  const Launch l(dev);
+  check("waits_q4_append", waits_q4_append(&c, count("rows", K.size(0)), K.data_ptr(), ks,
+                                           V.data_ptr(), vs, ints(slots), status, l.stream));
+  Py_RETURN_NONE;
+}
+
+// pool, slot_map, head_dim, status
+PyObject* q4_read(PyObject* const* a) {
+  int dev = -1;
+  const int64_t d = integer("head_dim", a[2]);
+  const waits_q4_cache c = cache(a[0], dev, d);
+  const at::Tensor& slots = dense("slot_map", a[1], at::kInt, dev);
+  const int64_t n = slots.numel();
+  vector("slot_map", a[1], at::kInt, dev, n);
+  uint32_t* status = status_word(a[3], dev);
+  const at::Tensor K = empty({n, c.num_kv_heads, d}, at::kBFloat16, dev);
+  const at::Tensor V = empty({n, c.num_kv_heads, d}, at::kBFloat16, dev);
+  const Launch l(dev);
+  check("waits_q4_read", waits_q4_read(&c, count("rows", n), ints(slots), K.data_ptr(),
+                                       V.data_ptr(), status, l.stream));
+  return tuple({K, V});
+}
+
+// K, V, cu_seqlens, idx, kept_len, block_table, pool, status
+PyObject* q4_compact(PyObject* const* a) {
+  int dev = -1;
+  const at::Tensor& K = dense("K", a[0], at::kBFloat16, dev);
+  const at::Tensor& V = dense("V", a[1], at::kBFloat16, dev);
+  if (K.dim() != 3) refuse("K must be [T, Hkv, d]");
+  if (V.sizes() != K.sizes()) refuse("V must have K's shape");
+  const int64_t T = K.size(0), Hkv = K.size(1), d = K.size(2);
+  const at::Tensor& idx = dense("idx", a[3], at::kInt, dev);
+  if (idx.dim() != 3 || idx.size(1) != Hkv) refuse("idx must be [nseq, Hkv, B]");
+  const int64_t nseq = idx.size(0), B = idx.size(2);
+  const at::Tensor& cu = vector("cu_seqlens", a[2], at::kInt, dev, nseq + 1);
+  const at::Tensor& kept = vector("kept_len", a[4], at::kInt, dev, nseq);
+  const at::Tensor& tab = table(a[5], dev, nseq);
+  const waits_q4_cache c = cache(a[6], dev, d);
+  uint32_t* status = status_word(a[7], dev);
+  const int32_t tokens = count("tokens", T), heads = count("heads", Hkv);
+  const waits_shape shape{count("sequences", nseq), tokens, tokens, heads, heads,
+                          count("head_dim", d), ints(cu)};
+  const Launch l(dev);
+  check("waits_q4_compact",
+        waits_q4_compact(&shape, K.data_ptr(), V.data_ptr(), ints(idx), ints(kept),
+                         count("B", B), &c, ints(tab), count("max_blocks", tab.size(1)), status,
+                         l.stream));
+  Py_RETURN_NONE;
+}
+
+// q, pool, block_table, cache_len, with_lse, workspace, status
+PyObject* q4_decode_attention(PyObject* const* a) {
+  int dev = -1;
+  const at::Tensor& q = dense("q", a[0], at::kBFloat16, dev);
+  if (q.dim() != 3) refuse("q must be [nseq, Hq, d]");
+  const int64_t nseq = q.size(0), Hq = q.size(1), d = q.size(2);
+  const waits_q4_cache c = cache(a[1], dev, d);
+  const at::Tensor& tab = table(a[2], dev, nseq);
+  const at::Tensor& len = vector("cache_len", a[3], at::kInt, dev, nseq);
+  const bool with_lse = truth(a[4]);
+  uint32_t* status = status_word(a[6], dev);
+  const int32_t ns = count("sequences", nseq), hq = count("heads", Hq);
+  at::Tensor ws;
+  if (a[5] == Py_None) {
+    size_t bytes = 0;
+    check("waits_q4_decode_workspace_size",
+          waits_q4_decode_workspace_size(&c, ns, hq, &bytes));
+    ws = empty({(int64_t)bytes}, at::kByte, dev);
+  } else {
+    ws = dense("workspace", a[5], at::kByte, dev);
+  }
+  const at::Tensor out = empty({nseq, Hq, d}, at::kBFloat16, dev);
+  at::Tensor lse;
+  if (with_lse) lse = empty({nseq, Hq}, at::kFloat, dev);
+  const Launch l(dev);
+  check("waits_q4_decode_attention",
+        waits_q4_decode_attention(&c, ns, hq, count("max_blocks", tab.size(1)), q.data_ptr(),
+                                  ints(tab), ints(len), out.data_ptr(),
+                                  with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+                                  ws.data_ptr(), (size_t)ws.numel(), status, l.stream));
+  if (with_lse) return tuple({out, lse});
+  return THPVariable_Wrap(out);
+}
+
+#define ENTRY(name, n) \
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<name, n>)), \
+   METH_FASTCALL, nullptr}
+
+PyMethodDef methods[] = {ENTRY(qk_norm_rope, 9),  ENTRY(cache_reserve, 9), ENTRY(cache_release, 7),
+                         ENTRY(q4_append, 5),     ENTRY(q4_read, 4),       ENTRY(q4_compact, 8),
+                         ENTRY(q4_decode_attention, 7), {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
+                      nullptr,               nullptr,    nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
