@@ -153,6 +153,23 @@ cudaError_t launch_rope_d(const RopeArgs& a, RopeParams& p, cudaStream_t st) {
   return a.interleaved ? go(rope_kernel<D, false, true>) : go(rope_kernel<D, false, false>);
 }
 
+// x / (2 pi) mod 1 as a fraction of 2^64, for |x| < 2^41: the 53-bit mantissa
+// times 128 bits of 1 / (2 pi), and of that product the 64 bits below the
+// point.  (Whole numbers: 64 conversions of long doubles cost 2 us a call.)
+uint64_t turn_fraction(double x) {
+  constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;   // 2^128 / (2 pi)
+  int e;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(x), &e), 53);
+  const int shift = 64 - (e - 53);                   // bits of the product below the wanted ones
+  const unsigned __int128 lo = (unsigned __int128)m * kLo, hi = (unsigned __int128)m * kHi;
+  const unsigned __int128 mid = (lo >> 64) + (uint64_t)hi;
+  const uint64_t limb[5] = {(uint64_t)lo, (uint64_t)mid, (uint64_t)((hi >> 64) + (mid >> 64)), 0, 0};
+  if (shift >= 192) return 0;
+  const int w = shift / 64, b = shift % 64;
+  const uint64_t f = b ? (limb[w] >> b) | (limb[w + 1] << (64 - b)) : limb[w];
+  return x < 0 ? 0 - f : f;                          // a negative one turns the other way
+}
+
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
@@ -173,13 +190,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   p.Hkv = a.Hkv;
   p.rot = a.rot;
   p.eps = a.eps;
-  for (int i = 0; i < a.rot / 2; ++i) {
-    // inv_freq / (2 pi) with a mantissa of 64 bits; its fraction as 0.64,
-    // modulo 2^64 (a negative frequency turns the other way)
-    const long double t = (long double)a.inv_freq[i] * 0.159154943091895335768883763372514362L;
-    const long double f = (t - (long double)(int64_t)t) * 18446744073709551616.0L;
-    p.turns[i] = f < 0 ? 0 - (uint64_t)-f : (uint64_t)f;
-  }
+  for (int i = 0; i < a.rot / 2; ++i) p.turns[i] = turn_fraction(a.inv_freq[i]);
   return a.d == 64 ? launch_rope_d<64>(a, p, st) : launch_rope_d<128>(a, p, st);
 }
 
