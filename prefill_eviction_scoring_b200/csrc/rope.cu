@@ -61,10 +61,40 @@ __global__ void __launch_bounds__(kRopeThreads)
   const bool turn = l < p.rot / 8;
   const int o1 = turn ? 4 * l : p.rot + 8 * (l - p.rot / 8);
   const int o2 = turn ? p.rot / 2 + 4 * l : o1 + 4;
+  // This warp's head rows, first those of q, then those of k, in batches of
+  // kAhead steps of kRows.  A batch is loaded while the one before is turned
+  // (the first while the angles are made).  An output may be its input: a
+  // warp's rows are its own, and every lane reads its values of a row before
+  // it writes them.
+  constexpr int kBatch = kRows * kAhead;
+  const int r0 = (int)(warp - t * p.warps_per_token) * p.rows_per_warp;
+  const int r1 = min(r0 + p.rows_per_warp, p.Hq + p.Hkv);
+  const int q0 = min(r0, p.Hq), q1 = min(r1, p.Hq), k0 = max(r0 - p.Hq, 0), k1 = r1 - p.Hq;
+  const int nq = (q1 - q0 + kBatch - 1) / kBatch;
+  const int n = nq + (k1 > k0 ? (k1 - k0 + kBatch - 1) / kBatch : 0);
+  const uint16_t *qsrc = p.q + t * p.qs, *ksrc = p.k + t * p.ks;
+  uint16_t *qdst = p.qo + t * p.qos, *kdst = p.ko + t * p.kos;
+  uint2 v[kAhead][2];
+  auto load = [&](int batch) {
+    const bool isq = batch < nq;
+    const uint16_t* src = isq ? qsrc : ksrc;
+    const int row0 = isq ? q0 + batch * kBatch : k0 + (batch - nq) * kBatch;
+    const int end = isq ? q1 : k1;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = row0 + i * kRows + sub;
+      v[i][0] = v[i][1] = make_uint2(0, 0);
+      if (row < end) {
+        v[i][0] = *reinterpret_cast<const uint2*>(src + (int64_t)row * D + o1);
+        v[i][1] = *reinterpret_cast<const uint2*>(src + (int64_t)row * D + o2);
+      }
+    }
+  };
+  const int pos = p.pos[t];
+  load(0);
   // pair e of this lane: half-split (o1 + e, o2 + e); interleaved
   // (o1, o1 + 1), (o1 + 2, o1 + 3), then the same from o2
   float cs[4], sn[4];
-  const int pos = p.pos[t];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     cs[e] = 1.f;
@@ -75,62 +105,55 @@ __global__ void __launch_bounds__(kRopeThreads)
       sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);
     }
   }
-  // Rows [r0, r1) of one tensor, kRows at once and kAhead of those in flight.
-  // An output may be its input: a warp's rows are its own, and every lane
-  // reads its values of a row before it writes them.
-  auto rows = [&](const uint16_t* src, uint16_t* dst, const uint16_t* weight, int r0, int r1) {
-    float w[8];
-    if (NORM) {
+  float w[8];
+  for (int batch = 0; batch < n; ++batch) {
+    const bool isq = batch < nq;
+    if (NORM && (batch == 0 || batch == nq)) {
+      const uint16_t* weight = isq ? p.qw : p.kw;
       unpack4(*reinterpret_cast<const uint2*>(weight + o1), w);
       unpack4(*reinterpret_cast<const uint2*>(weight + o2), w + 4);
     }
-    for (int row0 = r0; row0 < r1; row0 += kRows * kAhead) {
-      uint2 v[kAhead][2];
+    uint2 cur[kAhead][2];
+    if (NORM && batch > 0) load(batch);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int row = row0 + i * kRows + sub;
-        v[i][0] = v[i][1] = make_uint2(0, 0);
-        if (row < r1) {
-          v[i][0] = *reinterpret_cast<const uint2*>(src + (int64_t)row * D + o1);
-          v[i][1] = *reinterpret_cast<const uint2*>(src + (int64_t)row * D + o2);
-        }
+    for (int i = 0; i < kAhead; ++i) {
+      cur[i][0] = v[i][0];
+      cur[i][1] = v[i][1];
+    }
+    if (!NORM && batch + 1 < n) load(batch + 1);
+    uint16_t* dst = isq ? qdst : kdst;
+    const int row0 = isq ? q0 + batch * kBatch : k0 + (batch - nq) * kBatch;
+    const int end = isq ? q1 : k1;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = row0 + i * kRows + sub;
+      float x[8], y[8];
+      unpack4(cur[i][0], x);
+      unpack4(cur[i][1], x + 4);
+      if (NORM) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
       }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int row = row0 + i * kRows + sub;
-        float x[8], y[8];
-        unpack4(v[i][0], x);
-        unpack4(v[i][1], x + 4);
-        if (NORM) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int a = INTER ? 2 * e : e, b = INTER ? 2 * e + 1 : e + 4;
-          y[a] = x[a] * cs[e] - x[b] * sn[e];
-          y[b] = x[b] * cs[e] + x[a] * sn[e];
-        }
-        if (row < r1) {
-          *reinterpret_cast<uint2*>(dst + (int64_t)row * D + o1) =
-              make_uint2(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]));
-          *reinterpret_cast<uint2*>(dst + (int64_t)row * D + o2) =
-              make_uint2(pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int a = INTER ? 2 * e : e, b = INTER ? 2 * e + 1 : e + 4;
+        y[a] = x[a] * cs[e] - x[b] * sn[e];
+        y[b] = x[b] * cs[e] + x[a] * sn[e];
+      }
+      if (row < end) {
+        *reinterpret_cast<uint2*>(dst + (int64_t)row * D + o1) =
+            make_uint2(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]));
+        *reinterpret_cast<uint2*>(dst + (int64_t)row * D + o2) =
+            make_uint2(pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
       }
     }
-  };
-  const int r0 = (int)(warp - t * p.warps_per_token) * p.rows_per_warp;
-  const int r1 = min(r0 + p.rows_per_warp, p.Hq + p.Hkv);
-  if (r0 < p.Hq) rows(p.q + t * p.qs, p.qo + t * p.qos, p.qw, r0, min(r1, p.Hq));
-  if (r1 > p.Hq)
-    rows(p.k + t * p.ks, p.ko + t * p.kos, p.kw, max(r0 - p.Hq, 0), r1 - p.Hq);
+  }
 }
 
 template <int D>
