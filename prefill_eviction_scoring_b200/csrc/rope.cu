@@ -18,7 +18,10 @@
 namespace waits {
 namespace {
 
-constexpr int kRopeThreads = 256;
+// Small blocks: a warp lives for one token only, and a finished block of two
+// makes room at once (110 us for 32768 tokens of 32 + 8 heads against 119 with
+// blocks of eight warps).  At most 64 registers keep 32 warps on an SM.
+constexpr int kRopeThreads = 64;
 constexpr int kAhead = 4;   // steps of head rows whose loads a warp has in flight
 
 struct RopeParams {
@@ -47,7 +50,7 @@ __device__ inline void unpack4(uint2 v, float* x) {
 }
 
 template <int D, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, NORM ? 16 : 14)
     rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;           // lanes per row
   constexpr int kRows = 32 / kLanes;      // rows a warp handles at once
