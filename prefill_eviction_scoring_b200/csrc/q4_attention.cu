@@ -383,56 +383,60 @@ __global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs
   // copies a half tile, whose page it looks up one tile ahead.
   int p_left = 0;                          // tiles not yet issued
   if (run > warp) p_left = (int)((run - warp + kWarps - 1) / kWarps);
-  int p_s = s, p_g = g, p_nt = nt, p_tile = tile0, p_stage = 0, p_block = -1;
+  int p_s = s, p_g = g, p_n = tokens(s), p_nt = nt, p_tile = tile0, p_stage = 0, p_block = -1;
+  const int32_t* p_row = a.table + (int64_t)s * a.width;
   const int half = lane >> 4, hl = lane & 15;
   auto settle = [&]() {                    // bring p_tile into its item; load the half's block
-    while (p_tile >= p_nt) {
-      p_tile -= p_nt;
-      if (++p_g == Hkv) {
-        p_g = 0;
-        do ++p_s; while ((p_nt = tiles(p_s)) == 0);
-      }
+    if (p_tile >= p_nt) {
+      do {
+        p_tile -= p_nt;
+        if (++p_g == Hkv) {
+          p_g = 0;
+          do ++p_s; while ((p_n = tokens(p_s)) == 0);
+          p_nt = (int)(((int64_t)p_n + kTok - 1) / kTok);
+        }
+      } while (p_tile >= p_nt);
+      p_row = a.table + (int64_t)p_s * a.width;
     }
     const int j = p_tile * kTok + half * kSub;   // a tile's second half may lie past the end
-    p_block = j < tokens(p_s) ? __ldg(a.table + (int64_t)p_s * a.width + (j >> log_bs)) : -2;
+    p_block = j < p_n ? __ldg(p_row + (j >> log_bs)) : -2;
   };
   if (p_left > 0) {
     p_tile += warp;
     settle();
   }
-  // where a lane's 16-byte pieces of a half go: K rows and V rows in orders
-  // that keep the fragment reads free of bank conflicts
+  // Where a lane's 16-byte pieces hl, hl + 16, .. of a half come from and go:
+  // K rows and V rows in orders that keep the fragment reads free of bank
+  // conflicts.  K's row t goes to row t (d = 64: with bits 1 and 2 swapped),
+  // V's to row 4 (t % 4) + t / 4; d = 128 swaps the 32-byte halves of V's rows
+  // from token 8 on.
+  const size_t block_bytes = (size_t)Hkv * page_bytes;
+  const uint32_t v_range = (uint32_t)(page_bytes / 2);     // V's codes follow K's codes and scales
+  const uint8_t* pool = a.c.pool + hl * 16;
+  const int sc_which = hl >= D / 16, sc_ch = hl % (D / 16);
+  const int sc_src = (int)(sc_which * v_range + ((D / 2) << log_bs)) + (sc_ch - hl) * 16;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0]) + half * S::kHalf;
-  auto k_dst = [&](int id) -> uint32_t {
-    const int t = id / NG, ch = id % NG;
-    const int kr = D == 128 ? t : ((t & 9) | ((t & 4) >> 1) | ((t & 2) << 1));
-    return kr * (D / 2) + ch * 16;
-  };
-  auto v_dst = [&](int id) -> uint32_t {
-    const int t = id / NG, ch = id % NG;
-    const int vr = 4 * (t & 3) + (t >> 2);
-    return S::kCodes + vr * (D / 2) + (D == 128 ? ch ^ (2 * ((t >> 3) & 1)) : ch) * 16;
-  };
+  const int row0 = hl / NG, ch0 = hl % NG;
+  const uint32_t k_dst =
+      (D == 128 ? row0 : (row0 & 1) | ((row0 & 4) >> 1) | ((row0 & 2) << 1)) * (D / 2) + ch0 * 16;
+  const uint32_t v_dst = S::kCodes + (4 * (row0 & 3) + (row0 >> 2)) * (D / 2) + ch0 * 16;
+  const uint32_t sc_dst = 2 * S::kCodes + sc_which * S::kScales + sc_ch * 16;
   auto issue = [&]() {
     if (p_left > 0) {
       const bool ok = (unsigned)p_block < (unsigned)a.c.num_blocks;
       if (hl == 0) sm.page_ok[warp][p_stage][half] = ok;
       if (ok) {
-        const int off = (p_tile * kTok + half * kSub) & ((1 << log_bs) - 1);
-        const uint8_t* page = a.c.pool + ((size_t)p_block * Hkv + p_g) * page_bytes;
-        const uint8_t* kc = page + Q4Page<D>::code(0, log_bs, off) + hl * 16;
-        const uint8_t* vc = page + Q4Page<D>::code(1, log_bs, off) + hl * 16;
+        const uint32_t off = (p_tile * kTok + half * kSub) & ((1 << log_bs) - 1);
+        const uint8_t* page = pool + (uint32_t)p_block * block_bytes + p_g * (uint32_t)page_bytes;
+        const uint8_t* kc = page + off * (D / 2);
+        const uint8_t* vc = kc + v_range;
         const uint32_t dst = ring + p_stage * S::kTileBytes;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          cp_async16(dst + k_dst(hl + 16 * i), kc + i * 256);
-          cp_async16(dst + v_dst(hl + 16 * i), vc + i * 256);
+        for (int i = 0; i < D / 32; ++i) {             // rows 16 / NG further each
+          cp_async16(dst + k_dst + i * 256, kc + i * 256);
+          cp_async16(dst + (D == 128 && i >= 2 ? v_dst ^ 32 : v_dst) + i * 64, vc + i * 256);
         }
-        if (D == 128 || hl < D / 8) {
-          const int which = hl >= D / 16, ch = hl % (D / 16);
-          cp_async16(dst + 2 * S::kCodes + which * S::kScales + ch * 16,
-                     page + Q4Page<D>::scale(which, log_bs, off) + ch * 16);
-        }
+        if (D == 128 || hl < D / 8) cp_async16(dst + sc_dst, page + sc_src + off * (D / 16));
       } else if (a.status && p_block != -2 && hl == 0) {
         atomicOr(a.status, WAITS_DEV_BAD_INDEX);
       }
