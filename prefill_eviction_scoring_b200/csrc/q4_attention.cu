@@ -12,7 +12,7 @@
 // item in order.  So the workspace depends on the grid alone and the result
 // on nothing but the inputs.
 //
-// A warp takes every eighth tile of its CTA's run: it streams the tile's
+// A warp takes every 12th (or 8th) tile of its CTA's run: it streams the tile's
 // codes and scales into its own ring of shared memory (cp.async, kStages - 1
 // tiles ahead, across item boundaries), forms the logits and the weighted
 // sum with mma.m16n8k16 and keeps its own running maximum and sums; the
@@ -32,9 +32,7 @@
 namespace waits {
 namespace {
 
-constexpr int kWarps = 12;
 constexpr int kJoiners = 4;           // warps that add up an item's sums, in turn
-constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
 constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
@@ -142,8 +140,12 @@ __device__ inline float max4(float a, float b, float c, float d) {
 }
 
 // HEADS: query heads of a group that the kernel is built for, 4, 8 or 16.
+// Twelve warps at 168 registers; the sums of 16 heads of 128 dimensions need
+// more, and eight warps have them (69 us with twelve, which spill, 56
+// with eight: 64 sequences of 16384 tokens, 16 heads on one).
 template <int D, int HEADS>
 struct Smem {
+  static constexpr int kWarps = D == 128 && HEADS == 16 ? 8 : 12;
   static constexpr int kCodes = kSub * D / 2;           // bytes of a half tile's K (or V) codes
   static constexpr int kScales = kSub * D / 16;
   static constexpr int kHalf = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
@@ -230,10 +232,12 @@ __device__ inline int cta_of(int64_t unit, int64_t total, int ctas) {
 // use the columns twice: 0 - 3 weigh with V's scale of the even group, 4 - 7
 // with the odd group's.
 template <int D, int HEADS>
-__global__ void __launch_bounds__(kThreads, 1) q4_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
+    q4_decode_kernel(const DecodeArgs a) {
   constexpr int NG = D / 32, NW2 = D / 64, NT = HEADS == 16 ? 2 : 1;
   constexpr bool kTwice = HEADS == 4;
   using S = Smem<D, HEADS>;
+  constexpr int kWarps = S::kWarps, kThreads = 32 * kWarps;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -895,7 +899,8 @@ template <int D, int HEADS>
 cudaError_t launch_d(const DecodeArgs& a, int dev, int ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, HEADS>, dim3(ctas),
-                                          dim3(kThreads), sizeof(Smem<D, HEADS>), st, a);
+                                          dim3(32 * Smem<D, HEADS>::kWarps),
+                                          sizeof(Smem<D, HEADS>), st, a);
   if (err != cudaSuccess) return err;
   return launch_pdl(q4_join_kernel<D>, dim3(ctas), dim3(32 * a.G), 0, st, a);
 }

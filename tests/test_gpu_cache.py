@@ -15,11 +15,12 @@ value, half its eps; fp16 by 2^-11):
   addition); then one bf16 rounding.  The LSE has the logits' error alone.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
-import oracle
 from oracle import cache_oracle as co
 from prefill_eviction_scoring_b200 import _lib, api
 from prefill_eviction_scoring_b200 import workloads as wl
@@ -644,3 +645,284 @@ def test_other_stream():
         got = api.q4_decode_attention(q, pool, table, lens)
     s.synchronize()
     assert torch.equal(ref, got)
+
+
+# ------------------------------------------------------------------ calls at the edges
+
+@pytest.mark.parametrize("shift", [8, 16])
+def test_rows_on_sixteen_bytes(shift):
+    """Rows that start on 16 bytes but not on 32 take the narrower accesses."""
+    g = _gen(50)
+    buf = _bf(g, 40 * (2 * 128 + 8) + 64)
+    K = buf[shift:].as_strided((40, 2, 128), (264, 128, 1))
+    V = K.contiguous()
+    assert (K.data_ptr() % 32 == 0) == (shift == 16)
+    slots = torch.arange(40, dtype=torch.int32, device="cuda")
+    a, b = _pool(3, 2, 16, 128), _pool(3, 2, 16, 128)
+    api.q4_append(K, V, slots, a)
+    api.q4_append(V, V, slots, b)
+    assert torch.equal(a, b)
+    # read back through the C entry into outputs on 16 bytes
+    ref, _ = api.q4_read(a, slots, 128)
+    out = torch.full((2 * 40 * 256 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    c = _lib.Q4Cache(3, 16, 2, 128, a.data_ptr())
+    k0, v0 = shift, shift + 40 * 256 + 8
+    st = _lib.load().waits_q4_read(ctypes.byref(c), 40, slots.data_ptr(),
+                                   out.data_ptr() + 2 * k0, out.data_ptr() + 2 * v0, None,
+                                   torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for at in (k0, v0):
+        assert torch.equal(out[at:at + 40 * 256].view(40, 2, 128), ref)
+    rest = torch.ones_like(out, dtype=torch.bool)
+    rest[k0:k0 + 40 * 256] = rest[v0:v0 + 40 * 256] = False
+    assert (out[rest] == 7).all()
+
+
+@pytest.mark.parametrize("n", [148 * 8 * 32 // 8 + 5, 40000])
+def test_read_many_rows(n):
+    """Enough rows that a thread reads two back, with an odd number of them."""
+    g = _gen(51)
+    K, V = _bf(g, n, 1, 64), _bf(g, n, 1, 64)
+    blocks = n // 256 + 1
+    slots = torch.randperm(blocks * 256, generator=g, device="cuda")[:n].int()
+    pool = _pool(blocks, 1, 256, 64)
+    api.q4_append(K, V, slots, pool)
+    Kr, Vr = api.q4_read(pool, slots, 64)
+    for x, y in ((K, Kr), (V, Vr)):
+        assert np.array_equal(_f64(y), co.round_bf16(co.q4_value(*co.q4_quantise(_f64(x)))))
+
+
+@pytest.mark.parametrize("nseq,Hq,Hkv,d", [(33, 8, 2, 128), (32, 8, 2, 128), (700, 2, 1, 64),
+                                           (60, 64, 4, 128), (200, 28, 4, 64), (90, 32, 8, 128)])
+def test_attend_many_sequences(nseq, Hq, Hkv, d):
+    """Many short items per CTA, empty ones among them, on both planning paths."""
+    rng = np.random.default_rng(nseq)
+    lens = rng.integers(0, 260, nseq).tolist()
+    lens[nseq // 2] = 2500
+    g = _gen(nseq)
+    pool, table, kv = _fill(g, lens, Hkv, d, 16)
+    _check_attend(_bf(g, nseq, Hq, d), pool, table, lens, kv)
+
+
+def test_attend_all_empty():
+    q = _bf(_gen(1), 40, 8, 64)
+    for nseq in (1, 32, 40):
+        out, lse = api.q4_decode_attention(q[:nseq].contiguous(), _pool(2, 2, 16, 64),
+                                           _i32(np.full((nseq, 3), -1)), _i32([0] * nseq), True)
+        assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_attend_nan_key():
+    """A key that is not a number makes its head's sequence NaN, no other."""
+    g = _gen(52)
+    lens = [70, 70]
+    pool, table, _ = _fill(g, lens, 2, 64, 16)
+    K = _bf(g, 1, 2, 64)
+    V = K.clone()
+    K[0, 0, 3] = float("nan")
+    api.q4_append(K, V, (table[1, 1] * 16).view(1), pool)
+    out, lse = api.q4_decode_attention(_bf(g, 2, 4, 64), pool, table, _i32(lens), True)
+    assert torch.isnan(out[1, :2]).all() and torch.isnan(lse[1, :2]).all()
+    assert torch.isfinite(out[1, 2:]).all() and torch.isfinite(out[0]).all()
+    assert torch.isfinite(lse[1, 2:]).all() and torch.isfinite(lse[0]).all()
+
+
+def test_attend_zero_query_and_zero_cache():
+    """No logit differs: the output is the mean of V; zero V gives zeros."""
+    g = _gen(53)
+    pool, table, kv = _fill(g, [333], 1, 128, 16)
+    out, lse = api.q4_decode_attention(torch.zeros((1, 4, 128), dtype=torch.bfloat16,
+                                                   device="cuda"), pool, table, _i32([333]), True)
+    ref = kv[0][1][0].mean(0)
+    assert np.all(np.abs(_f64(out[0, 0]) - ref) <= BF * np.abs(ref) + 2.0 ** -10 * 3)
+    assert np.allclose(_f64(lse), np.log(333.0), atol=2.0 ** -13)
+    zero = torch.zeros_like(pool)
+    out, lse = api.q4_decode_attention(_bf(g, 1, 4, 128), zero, table, _i32([333]), True)
+    assert not out.any() and np.allclose(_f64(lse), np.log(333.0), atol=2.0 ** -13)
+
+
+def test_pool_past_four_gigabytes():
+    """Blocks whose bytes lie past 32 bits."""
+    Hkv, d, bs = 8, 128, 256
+    blocks = 2 ** 32 // (Hkv * bs * d * 9 // 8) + 40
+    pool = torch.empty((blocks, Hkv, bs * d * 9 // 8), dtype=torch.uint8, device="cuda")
+    g = _gen(54)
+    n = 600
+    K, V = _bf(g, n, Hkv, d), _bf(g, n, Hkv, d)
+    table = _i32([[blocks - 1, 3, blocks - 20]])
+    j = torch.arange(n, device="cuda")
+    slots = (table[0, j // bs] * bs + j % bs).int()
+    api.q4_append(K, V, slots, pool)
+    Kr, Vr = api.q4_read(pool, slots, d)
+    kv = []
+    for x, y in ((K, Kr), (V, Vr)):
+        val = co.q4_value(*co.q4_quantise(_f64(x)))
+        assert np.array_equal(_f64(y), co.round_bf16(val))
+        kv.append(val.transpose(1, 0, 2))
+    _check_attend(_bf(g, 1, 32, d), pool, table, [n], [kv])
+
+
+def test_rope_offsets_past_32_bits():
+    stride = 2 ** 27
+    g = _gen(55)
+    T = 18
+    big = torch.empty(stride * (T - 1) + 4 * 128, dtype=torch.bfloat16, device="cuda")
+    q = big.as_strided((T, 4, 128), (stride, 128, 1))
+    src = _bf(g, T, 4, 128)
+    q.copy_(src)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 1000
+    inv = api.rotary_inv_freq(128, 1e6)
+    k = _bf(g, T, 2, 128)
+    ref = api.qk_norm_rope(src, k, pos, inv)
+    got = api.qk_norm_rope(q, k, pos, inv, out=(q, torch.empty_like(k)))
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    pool = _pool(2, 4, 16, 128)
+    pool2 = pool.clone()
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    api.q4_append(q, q, slots, pool)
+    api.q4_append(ref[0], ref[0], slots, pool2)
+    assert torch.equal(pool, pool2)
+
+
+def test_two_caches_on_two_streams():
+    """Calls with their own workspaces may overlap."""
+    g = _gen(56)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    sets, refs = [], []
+    for i in range(2):
+        lens = [3000 + 100 * i, 17, 900]
+        pool, table, kv = _fill(g, lens, 4, 128, 16)
+        q = _bf(g, 3, 16, 128)
+        sets.append((q, pool, table, _i32(lens)))
+        refs.append(api.q4_decode_attention(*sets[-1], True))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[i].append(api.q4_decode_attention(*sets[i], True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, refs[i][0]) and torch.equal(lse, refs[i][1])
+
+
+def test_two_graphs_share_a_workspace_in_turn():
+    g = _gen(57)
+    lens = [1500, 40]
+    pool, table, kv = _fill(g, lens, 2, 64, 16)
+    q = [_bf(g, 2, 8, 64) for _ in range(2)]
+    ws = torch.empty(api.q4_decode_workspace_bytes(pool, 2, 8, 64), dtype=torch.uint8,
+                     device="cuda")
+    L = _i32(lens)
+    ref = [api.q4_decode_attention(x, pool, table, L, True) for x in q]
+    graphs, res = [], []
+    for x in q:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            res.append(api.q4_decode_attention(x, pool, table, L, True, workspace=ws))
+        graphs.append(cg)
+    for _ in range(3):
+        for cg in graphs:
+            cg.replay()
+    torch.cuda.synchronize()
+    for (a, b), (c, d) in zip(ref, res):
+        assert torch.equal(a, c) and torch.equal(b, d)
+    # the lengths are read when the graph runs, not when it is captured
+    L.copy_(_i32([3, 0]))
+    graphs[0].replay()
+    out, lse = api.q4_decode_attention(q[0], pool, table, _i32([3, 0]), True)
+    assert torch.equal(res[0][0], out) and torch.equal(res[0][1], lse)
+
+
+def test_captured_append_rope_reserve_release():
+    g = _gen(58)
+    cache = api.Q4Cache(4, 8, 2, 64, num_blocks=30, max_blocks=6, block_size=16)
+    ref = api.Q4Cache(4, 8, 2, 64, num_blocks=30, max_blocks=6, block_size=16)
+    new, ended = _i32([3, 0, 1, 5]), _i32([0, 1, 0, 0])
+    K, V = _bf(g, 9, 2, 64), _bf(g, 9, 2, 64)
+    cg = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(cg):
+        slots, cu = cache.reserve(new, 9)
+        cache.append(K, V, slots)
+        cache.release(ended)
+    for i in range(8):
+        new.copy_(_i32([3, 0, 1, 5] if i % 2 else [2, 4, 3, 0]))
+        ended.copy_(_i32([0, 1, 0, i == 5]))
+        cg.replay()
+        s, c = ref.reserve(new, 9)
+        ref.append(K, V, s)
+        ref.release(ended)
+        assert torch.equal(slots, s) and torch.equal(cu, c)
+    for name in ("pool", "block_table", "cache_len", "free_list", "free_count", "status"):
+        assert torch.equal(getattr(cache, name), getattr(ref, name)), name
+
+
+def test_refused_tensors():
+    """What the binding refuses once tensors are on the GPU."""
+    g = _gen(59)
+    pool = _pool(4, 2, 16, 64)
+    K = _bf(g, 5, 2, 64)
+    slots = torch.arange(5, dtype=torch.int32, device="cuda")
+    table, lens = _i32([[0, 1]]), _i32([20])
+    q = _bf(g, 1, 4, 64)
+    inv = api.rotary_inv_freq(64, 1e4)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    bad = [
+        (lambda: api.q4_append(K, K, slots.long(), pool), "slot_map must be torch.int32"),
+        (lambda: api.q4_append(K, K, slots[:4], pool), "slot_map"),
+        (lambda: api.q4_append(K.float(), K, slots, pool), "K must be torch.bfloat16"),
+        (lambda: api.q4_append(K, K[:, :1], slots, pool), "V must have K's shape"),
+        (lambda: api.q4_append(K[:, :1].contiguous(), K[:, :1].contiguous(), slots, pool),
+         "pool must have K's heads"),
+        (lambda: api.q4_append(K.transpose(0, 1), K.transpose(0, 1), slots, pool), "contiguous"),
+        (lambda: api.q4_append(K, K, slots, pool[:, :, :-8].contiguous()), "whole number of tokens"),
+        (lambda: api.q4_append(K, K, slots, pool.view(4, -1)), "pool must be uint8"),
+        (lambda: api.q4_append(K, K, slots, pool, status=slots), "status must hold one"),
+        (lambda: api.q4_append(K, K, slots.cpu(), pool), "slot_map must be a CUDA tensor"),
+        (lambda: api.q4_read(pool, slots.view(5, 1), 64), "slot_map"),
+        (lambda: api.q4_decode_attention(q, pool, table.view(2, 1), lens), "block_table must be"),
+        (lambda: api.q4_decode_attention(q, pool, table, lens.view(1, 1)), "cache_len"),
+        (lambda: api.q4_decode_attention(q[0], pool, table, lens), "q must be"),
+        (lambda: api.q4_decode_attention(q, pool, table, lens,
+                                         workspace=torch.empty(99, device="cuda")), "workspace"),
+        (lambda: api.qk_norm_rope(K, K[:4], pos, inv), "k must be"),
+        (lambda: api.qk_norm_rope(K, K, pos[:4], inv), "positions"),
+        (lambda: api.qk_norm_rope(K, K, pos, inv.float()), "inv_freq"),
+        (lambda: api.qk_norm_rope(K, K, pos, inv.cuda()), "inv_freq"),
+        (lambda: api.qk_norm_rope(K, K, pos, inv, q_weight=K[0, 0]), "come together"),
+        (lambda: api.qk_norm_rope(K, K, pos, inv, out=(K, K[:, :1])), "out must have"),
+        (lambda: api.cache_reserve(lens, lens, table, slots, slots, block_size=16, max_new=3),
+         "free_count must hold one"),
+        (lambda: api.cache_reserve(lens, lens, table, slots, slots[:1], block_size=16,
+                                   max_new=-3), "max_new"),
+    ]
+    for call, text in bad:
+        with pytest.raises(ValueError, match=text):
+            call()
+    for call, status in [
+            (lambda: api.cache_reserve(lens, lens, table, slots, slots[:1], block_size=24,
+                                       max_new=3), 3),
+            (lambda: api.q4_decode_attention(q, pool, table, lens, workspace=torch.empty(
+                16, dtype=torch.uint8, device="cuda")), 4),
+            (lambda: api.q4_decode_attention(_bf(g, 1, 3, 64), pool, table, lens), 2),
+            (lambda: api.q4_decode_attention(_bf(g, 1, 34, 64), pool, table, lens), 3),
+            (lambda: api.qk_norm_rope(K, K, pos, api.rotary_inv_freq(128, 1e4)), 2),
+            (lambda: api.qk_norm_rope(K, K, pos, inv * 1e13), 1),
+            (lambda: api.qk_norm_rope(K, K, pos, inv, q_weight=K[0, 0], k_weight=K[0, 0],
+                                      eps=-1.0), 1)]:
+        with pytest.raises(_lib.WaitsError) as e:
+            call()
+        assert e.value.status == status
+    torch.cuda.synchronize()
+
+
+def test_empty_calls():
+    pool = _pool(2, 2, 16, 64)
+    none = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(0, dtype=torch.int32, device="cuda")
+    before = pool.clone()
+    api.q4_append(none, none, slots, pool)
+    K, V = api.q4_read(pool, slots, 64)
+    assert K.shape == V.shape == (0, 2, 64) and torch.equal(pool, before)
