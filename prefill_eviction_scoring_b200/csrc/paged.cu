@@ -4,10 +4,14 @@
 // blocks; an exclusive prefix sum over the sequences says which blocks of the
 // free stack are its own, a prefix sum of the new tokens where its slots
 // start.  Latency bounds it: a decode step moves a few hundred bytes.  So one
-// launch of one cluster of 8 CTAs does all of it: every CTA repeats the
-// (cheap) prefix sums in its shared memory, writes its share of the slots,
-// and after a cluster barrier, when no CTA reads the old lengths any more,
-// the first one updates lengths and count in place.
+// launch does all of it, of one CTA for up to 4096 slots (64 sequences, one
+// token each: 4.9 us on the GPU, against 6.1 with a cluster) and of a cluster
+// of 8 for more (8 prompts, 131072 slots, 0.5 MB: 8.9 us): every CTA repeats
+// the (cheap) prefix sums in its shared memory and writes its share of the
+// slots, and after a barrier, when nobody reads the old lengths any more, the
+// first one updates lengths and count in place.  A thread makes four
+// neighbouring slots, one 16-byte store, with one lookup of their block where
+// they share it.
 #include <cooperative_groups.h>
 
 #include "waits_internal.cuh"

@@ -13,13 +13,25 @@
 // on nothing but the inputs.
 //
 // A warp takes every 12th (or 8th) tile of its CTA's run: it streams the tile's
-// codes and scales into its own ring of shared memory (cp.async, kStages - 1
-// tiles ahead, across item boundaries), forms the logits and the weighted
-// sum with mma.m16n8k16 and keeps its own running maximum and sums; the
-// CTA's warps meet only at the end of an item.  tcgen05 would need the
+// codes and scales into its own ring of shared memory (cp.async, one tile
+// ahead, across item boundaries), forms the logits and the weighted sum with
+// mma.m16n8k16 and keeps its own running maximum and sums; at the end of an
+// item it leaves them in shared memory and goes on.  tcgen05 would need the
 // decoded operands in shared memory, 3.5 bytes written for each byte read;
 // here the fragments are decoded in registers: the page's byte order makes
 // each lane's codes contiguous and in fragment order.
+//
+// What it measured (B200; a call's two kernels in a graph, us): 32 sequences of
+// 16384 tokens, 32 / 8 heads of 128 (604 MB) 112, 5.4 TB/s or 82 % of a plain
+// copy's rate; 8 of them 37; one of 131072 37; one of 2064 9.0; 8 ragged ones
+// of 4096 to 16384, 28 / 4 heads, 19; 64 of about 2050 45.  Large calls spend
+// about as long on instructions as HBM on the bytes: without its loads the
+// kernel takes 92 of 112 us, and instructions, not latency, fill that (8, 12
+// and 16 warps are within 5 %).  Small ones are bound by the chain length ->
+// block -> tile -> sums -> join, about 1 us each.  Tried and slower: three or
+// four tiles ahead (no change), 16 warps at 128 registers (5 %), barriers that
+// keep a CTA's warps abreast (3 %), tokens as columns of the first product (a
+// third more mma instructions, 9 %).
 //
 // Exactness: e2m1 codes are exact in fp16; q is scaled by a power of two
 // into fp16's range (exact above 2^-24 of its largest value); group sums are
@@ -36,8 +48,11 @@ constexpr int kJoiners = 4;           // warps that add up an item's sums, in tu
 constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
 constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
-constexpr int kMinTiles = 8;          // tiles per CTA, where there are few
-constexpr int kEndTiles = 60;         // what the end of an item inside a run may cost, in tiles
+constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 9.9 us for 9.0 on 1 x 2064)
+// What the end of an item inside a run may cost, in tiles of the run: measured
+// at 20, 60 and 100 on 8 sequences of 4096 tokens (17.6, 16.6, 16.6 us), of 2064
+// (14.8, 12.5, 12.5) and of 1000 to 16384 (33.9, 33.9, 37.3).
+constexpr int kEndTiles = 60;
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
 

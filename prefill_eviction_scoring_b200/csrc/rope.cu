@@ -2,7 +2,10 @@
 //
 // Per token and head row x: y = w x / sqrt(mean x^2 + eps), then each pair of
 // the first `rot` dimensions turns by angle p * inv_freq[i].  Every value is
-// read once and written once, so HBM bounds it: 4 bytes a value.
+// read once and written once, so HBM bounds it: 4 bytes a value.  32768
+// tokens of 32 + 8 heads of 128 dimensions (671 MB) take 110 us, 6.1 TB/s or
+// 93 % of a plain copy's rate; 7001 tokens of 32 + 8 heads of 64 without norm
+// (72 MB, which fits L2) 13.3 us; a step of 8 tokens 3.1 us, a launch's latency.
 //
 // A row is d/8 lanes; a lane owns 4 + 4 values, the two halves of four pairs
 // (dimensions 4l.. and rot/2 + 4l.. ; interleaved pairs lie inside a half),
@@ -13,6 +16,9 @@
 // The angle in turns is p * inv_freq / (2 pi) mod 1.  As a 64-bit fraction of
 // a turn the product wraps exactly, whatever the position: no reduction, no
 // fp64.  The top 32 bits go through sincospi in fp32.
+//
+// 8 + 8 values per lane and 16-byte accesses were slower (139 against 119 us
+// then): twice the registers for angles and rows in flight, half the warps.
 #include "waits_internal.cuh"
 
 namespace waits {

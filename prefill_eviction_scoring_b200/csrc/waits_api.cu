@@ -265,8 +265,9 @@ const char* waits_strerror(waits_status st) {
     case WAITS_OK: return "ok";
     case WAITS_ERR_ARG: return "invalid argument (null, misaligned, or a/b/R/B out of range)";
     case WAITS_ERR_SHAPE: return "invalid or inconsistent shape";
-    case WAITS_ERR_UNSUPPORTED: return "unsupported configuration (head_dim must be 64 or 128, G <= 128)";
-    case WAITS_ERR_WORKSPACE: return "workspace missing or smaller than waits_workspace_size()";
+    case WAITS_ERR_UNSUPPORTED: return "unsupported configuration (head_dim must be 64 or 128, the "
+                                      "heads per group, sequences and block size within the call's limits)";
+    case WAITS_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than its size call says";
     case WAITS_ERR_CUDA: return "a CUDA runtime call failed";
     case WAITS_ERR_TIMEOUT: return "a bounded device-side wait expired";
     case WAITS_ERR_DEVICE: return "device-side error (see WAITS_DEV_* status bits)";
