@@ -196,7 +196,7 @@ bool wide_rows(const void* p, int64_t stride) {
 // Block (rows, head): thread (row, t) takes K and V of one token and head.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-    append_kernel(Q4Pool c, int n, const uint16_t* __restrict__ K, int64_t ks,
+    q4_append_kernel(Q4Pool c, int n, const uint16_t* __restrict__ K, int64_t ks,
                   const uint16_t* __restrict__ V, int64_t vs, const int32_t* __restrict__ slots,
                   bool wide, uint32_t* status) {
   constexpr int kT = D / 16;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads)
 // Block (slots j, (sequence, head) sg): thread (j, t).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-    compact_kernel(Q4Pool c, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
+    q4_compact_kernel(Q4Pool c, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
                    const int32_t* __restrict__ cu, const int32_t* __restrict__ idx,
                    const int32_t* __restrict__ kept_len, int nseq, int T, int B,
                    const int32_t* __restrict__ table, int width, bool wide, uint32_t* status) {
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads)
 // ROWS: rows a thread reads back at once, 2 where there are blocks enough.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
-    read_kernel(Q4Pool c, int n, const int32_t* __restrict__ slots, uint16_t* __restrict__ K,
+    q4_read_kernel(Q4Pool c, int n, const int32_t* __restrict__ slots, uint16_t* __restrict__ K,
                 uint16_t* __restrict__ V, bool wide, uint32_t* status) {
   constexpr int kT = D / 16;
   pdl_allow_next();
@@ -310,7 +310,7 @@ unsigned blocks_for(int64_t rows, int d, int per = 1) {
 cudaError_t launch_q4_append(const Q4Pool& c, int n, const uint16_t* K, int64_t ks,
                              const uint16_t* V, int64_t vs, const int32_t* slots,
                              uint32_t* status, cudaStream_t st) {
-  auto kernel = c.d == 64 ? append_kernel<64> : append_kernel<128>;
+  auto kernel = c.d == 64 ? q4_append_kernel<64> : q4_append_kernel<128>;
   return launch_pdl(kernel, dim3(blocks_for(n, c.d), c.Hkv), dim3(kThreads), 0, st, c, n, K, ks,
                     V, vs, slots, wide_rows(K, ks) && wide_rows(V, vs), status);
 }
@@ -319,8 +319,8 @@ cudaError_t launch_q4_read(const Q4Pool& c, int n, const int32_t* slots, uint16_
                            uint32_t* status, cudaStream_t st) {
   // two rows per thread once one row's blocks would fill the SMs (8 each)
   const int per = (int64_t)blocks_for(n, c.d) * c.Hkv > 148 * 8 ? 2 : 1;
-  auto kernel = c.d == 64 ? (per == 2 ? read_kernel<64, 2> : read_kernel<64, 1>)
-                          : (per == 2 ? read_kernel<128, 2> : read_kernel<128, 1>);
+  auto kernel = c.d == 64 ? (per == 2 ? q4_read_kernel<64, 2> : q4_read_kernel<64, 1>)
+                          : (per == 2 ? q4_read_kernel<128, 2> : q4_read_kernel<128, 1>);
   return launch_pdl(kernel, dim3(blocks_for(n, c.d, per), c.Hkv), dim3(kThreads), 0, st, c, n,
                     slots, K, V, wide_rows(K, 0) && wide_rows(V, 0), status);
 }
@@ -330,7 +330,7 @@ cudaError_t launch_q4_compact(const Q4Pool& c, const uint16_t* K, const uint16_t
                               int nseq, int T, int B, const int32_t* table, int width,
                               uint32_t* status, cudaStream_t st) {
   const int64_t pairs = (int64_t)nseq * c.Hkv;
-  auto kernel = c.d == 64 ? compact_kernel<64> : compact_kernel<128>;
+  auto kernel = c.d == 64 ? q4_compact_kernel<64> : q4_compact_kernel<128>;
   return launch_pdl(kernel, dim3(blocks_for(B, c.d), (unsigned)(pairs < 65535 ? pairs : 65535)),
                     dim3(kThreads), 0, st, c, K, V, cu, idx, kept_len, nseq, T, B, table, width,
                     wide_rows(K, 0) && wide_rows(V, 0), status);
