@@ -16,7 +16,7 @@
 // of the page's byte order, two bytes each; pairs of threads trade half of
 // theirs and store whole words.  Appending 16001 rows of 4 heads (42 MB) and
 // reading them back takes 18.0 us, 25.0 us with 8 dimensions per thread and
-// divisions; the instructions, more than 160 for 32 values, and the latency of
+// divisions; the instructions, about 340 for 32 values, and the latency of
 // slot, then row, bound it before HBM does.
 #include "q4.cuh"
 
