@@ -33,18 +33,6 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Two values -> two e2m1 codes (lo in the low nibble): to nearest, ties to
-// the even code, saturating at 6.
-__device__ inline uint32_t e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The four bytes of w, two e2m1 codes each -> four half pairs (exact).
 __device__ inline void e2m1_to_half(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"

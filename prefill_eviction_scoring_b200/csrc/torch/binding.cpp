@@ -13,10 +13,12 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
 
 #include "waits.h"
 
@@ -179,11 +181,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return F(args);
   } catch (const PythonError&) {
     return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  } catch (...) {   // torch's own, out of memory among them, as torch raises them
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }
