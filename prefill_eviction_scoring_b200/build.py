@@ -84,7 +84,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *(f"-isystem{p}" for p in inc), BINDING_SRC, "-o", tmp,
           *(f"-L{p}" for p in cpp_extension.library_paths()), f"-L{PKG}", "-l:libwaits.so",
-          "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+          "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
           "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, BINDING)
     return BINDING

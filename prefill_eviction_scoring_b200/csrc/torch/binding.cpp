@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -19,6 +19,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
+#include <optional>
 
 #include "waits.h"
 
@@ -134,8 +135,9 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
+// (Past the dispatcher, which costs about as much as the allocation.)
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
+  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, dev), std::nullopt);
 }
 
 int32_t* ints(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
