@@ -10,7 +10,9 @@
 // output it writes, and at most two parts of items, whose (weighted sum,
 // maximum, sum) go to the workspace; a second kernel joins the parts of an
 // item in order.  So the workspace depends on the grid alone and the result
-// on nothing but the inputs.
+// on nothing but the inputs.  Items that are short by what the table can hold,
+// and few, skip all that: each has a cluster of 1 to 8 CTAs, which join their
+// sums through shared memory.
 //
 // A warp takes every 12th (or 8th) tile of its CTA's run: it streams the tile's
 // codes and scales into its own ring of shared memory (cp.async, one tile
@@ -23,7 +25,7 @@
 //
 // What it measured (B200; a call's two kernels in a graph, us): 32 sequences of
 // 16384 tokens, 32 / 8 heads of 128 (604 MB) 112, 5.4 TB/s or 82 % of a plain
-// copy's rate; 8 of them 37; one of 131072 37; one of 2064 9.0; 8 ragged ones
+// copy's rate; 8 of them 37; one of 131072 37; one of 2064 6.9; 8 ragged ones
 // of 4096 to 16384, 28 / 4 heads, 19; 64 of about 2050 45.  Large calls spend
 // about as long on instructions as HBM on the bytes: without its loads the
 // kernel takes 92 of 112 us, and instructions, not latency, fill that (8, 12
@@ -38,6 +40,8 @@
 // scaled in fp32.  The weights p_j * scale_jg enter the second product in
 // fp16 (2^-11 relative; bf16 would give 2^-8), after a power of two per warp
 // and group keeps them below 2^14 and V's largest scale near 1.
+#include <cooperative_groups.h>
+
 #include "q4.cuh"
 #include "sm100.cuh"
 
@@ -48,11 +52,13 @@ constexpr int kJoiners = 4;           // warps that add up an item's sums, in tu
 constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
 constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
-constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 9.9 us for 9.0 on 1 x 2064)
+constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 9.9 us for 9.0 on 1 x 2064
+                                      // without a cluster)
 // What the end of an item inside a run may cost, in tiles of the run: measured
 // at 20, 60 and 100 on 8 sequences of 4096 tokens (17.6, 16.6, 16.6 us), of 2064
 // (14.8, 12.5, 12.5) and of 1000 to 16384 (33.9, 33.9, 37.3).
 constexpr int kEndTiles = 60;
+constexpr int kMaxCluster = 8;        // CTAs of an item's cluster
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
 
@@ -63,6 +69,7 @@ struct Desc {       // the item whose parts begin with this CTA's last one
 struct DecodeArgs {
   Q4Pool c;
   int nseq, Hq, G, width;
+  int cluster;        // CTAs per item where the items have clusters of their own, else 0
   const uint16_t* q;
   const int32_t *table, *len;
   uint16_t* out;
@@ -172,8 +179,8 @@ struct Smem {
   float m[kSlots][kWarps][HEADS], l[kSlots][kWarps][HEADS];
   uint64_t full[kSlots], free[kSlots];
   int32_t page_ok[kWarps][kStages][2];
+  float all_o[HEADS][D], all_m[HEADS], all_l[HEADS];    // the CTA's sums, for its cluster
   int64_t scan[kWarps];
-  int64_t total;
   int64_t where[2];                                     // sequence of the run's start, units before it
 };
 
@@ -246,7 +253,7 @@ __device__ inline int cta_of(int64_t unit, int64_t total, int ctas) {
 // rows are dimensions and whose columns are the heads again.  Up to 4 heads
 // use the columns twice: 0 - 3 weigh with V's scale of the even group, 4 - 7
 // with the odd group's.
-template <int D, int HEADS>
+template <int D, int HEADS, bool CLUSTER>
 __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
     q4_decode_kernel(const DecodeArgs a) {
   constexpr int NG = D / 32, NW2 = D / 64, NT = HEADS == 16 ? 2 : 1;
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
   };
   auto tiles = [&](int s) -> int { return (int)(((int64_t)tokens(s) + kTok - 1) / kTok); };
 
-  if (tid == 0) a.desc[blockIdx.x].parts = 0;
+  if (!CLUSTER && tid == 0) a.desc[blockIdx.x].parts = 0;
   // empty sequences, shared among the CTAs
   auto zero_empty = [&]() {
     for (int s = blockIdx.x; s < a.nseq; s += gridDim.x) {
@@ -294,7 +301,22 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
   int64_t run, total = 0, u0 = 0;          // u0: tiles before the run
   int ctas = 0, parts = 0;                 // parts: CTAs per item, 0 where runs cross items
   const int grid = gridDim.x, me = blockIdx.x;
-  if (a.nseq <= 32) {
+  const int mine_of = CLUSTER ? me % a.cluster : 0;   // this CTA's place among its item's
+  if (CLUSTER) {
+    const int it = me / a.cluster;
+    s = it / Hkv;
+    g = it - s * Hkv;
+    nt = tiles(s);
+    tile0 = (int)split(nt, mine_of, a.cluster);
+    run = split(nt, mine_of + 1, a.cluster) - tile0;   // may be none
+    for (int i = tid; i < HEADS; i += kThreads) {
+      sm.all_m[i] = -INFINITY;
+      sm.all_l[i] = 0.f;
+    }
+    if (run == 0)
+      for (int i = tid; i < HEADS * D; i += kThreads) sm.all_o[i / D][i % D] = 0.f;
+    __syncthreads();
+  } else if (a.nseq <= 32) {
     // every warp by itself, a lane per sequence
     const int mine = lane < a.nseq ? tiles(lane) : 0;
     const int items = __popc(__ballot_sync(0xffffffffu, mine > 0)) * Hkv;
@@ -467,10 +489,10 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
     }
     cp_async_commit();
   };
-  load_q(s, g);
+  if (!CLUSTER || run > 0) load_q(s, g);
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) issue();
-  zero_empty();
+  if (!CLUSTER) zero_empty();
 
   // ---- the run, item by item
   int stage = 0, item = 0;
@@ -813,7 +835,13 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
           acc.z = fmaf(x.z, f, acc.z);
           acc.w = fmaf(x.w, f, acc.w);
         }
-        if (whole) {
+        if (CLUSTER) {
+          *reinterpret_cast<float4*>(&sm.all_o[h][d4]) = acc;
+          if (d4 == 0) {
+            sm.all_m[h] = M;
+            sm.all_l[h] = L;
+          }
+        } else if (whole) {
           const size_t row = (size_t)s * a.Hq + (size_t)g * G + h;
           const float inv = L == 0.f ? 0.f : 1.f / L;
           *reinterpret_cast<uint2*>(a.out + row * D + d4) =
@@ -829,7 +857,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
         }
       }
       // the first part of an item that goes on in the next CTAs
-      if (!whole && tile0 == 0 && lane == 0 && warp % kJoiners == 0) {
+      if (!CLUSTER && !whole && tile0 == 0 && lane == 0 && warp % kJoiners == 0) {
         const int all = parts ? parts : cta_of(u0 + u + nt - 1, total, ctas) - me + 1;
         a.desc[me] = Desc{s, g, all, first ? 0 : 1};
       }
@@ -845,6 +873,42 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
     nt = next_nt;
   }
   cp_async_wait<0>();
+  if (CLUSTER) {
+    // every CTA joins its share of the item's values from all CTAs' sums
+    auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    const int n = a.cluster;
+    for (int i = tid * n + mine_of; i < G * (D / 4); i += kThreads * n) {
+      const int h = i / (D / 4), d4 = 4 * (i % (D / 4));
+      float m[kMaxCluster], l[kMaxCluster];
+      float4 x[kMaxCluster];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        m[c] = -INFINITY;
+        if (c < n) {
+          m[c] = *cluster.map_shared_rank(&sm.all_m[h], c);
+          l[c] = *cluster.map_shared_rank(&sm.all_l[h], c);
+          x[c] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.all_o[h][d4], c));
+        }
+        M = fmaxf(M, m[c]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c)
+        if (c < n) {
+          const float f = m[c] == -INFINITY ? 0.f : exp2f(m[c] - M);
+          L = fmaf(l[c], f, L);
+          Floats<4>::add(acc, x[c], f);
+        }
+      const size_t row = (size_t)s * a.Hq + (size_t)g * G + h;
+      Floats<4>::scale(acc, L == 0.f ? 0.f : 1.f / L);
+      Floats<4>::store(a.out + row * D + d4, acc);
+      if (a.lse && d4 == 0)
+        a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+    cluster.sync();                                    // nobody reads this CTA's sums any more
+  }
 }
 
 // Joins the parts of an item: a CTA per CTA of the first kernel, a warp per
@@ -910,12 +974,61 @@ __global__ void __launch_bounds__(512) q4_join_kernel(const DecodeArgs a) {
 // The CTAs that the workspace has room for: one on every SM of a B200.
 constexpr int kMaxCtas = 148;
 
+// Clusters of 2^log_c CTAs that the current device runs at once (one CTA per
+// SM; 148, 74, 33 and 15 of them on a B200), asked once per device; 0 where it cannot.
 template <int D, int HEADS>
-cudaError_t launch_d(const DecodeArgs& a, int dev, int ctas, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, HEADS>, dim3(ctas),
-                                          dim3(32 * Smem<D, HEADS>::kWarps),
-                                          sizeof(Smem<D, HEADS>), st, a);
+int clusters_at_once(int dev, int log_c) {
+  static std::atomic<int> known[64][4];              // one more than the number
+  if (dev >= 64) return 0;
+  int n = known[dev][log_c].load(std::memory_order_relaxed) - 1;
+  if (n >= 0) return n;
+  using S = Smem<D, HEADS>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1 << log_c);
+  cfg.blockDim = dim3(32 * S::kWarps);
+  cfg.dynamicSmemBytes = sizeof(S);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1u << log_c;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(q4_decode_kernel<D, HEADS, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)sizeof(S)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, q4_decode_kernel<D, HEADS, true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][log_c].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int D, int HEADS>
+cudaError_t launch_d(DecodeArgs a, int dev, int ctas, cudaStream_t st) {
+  using S = Smem<D, HEADS>;
+  static std::atomic<uint64_t> done{0}, done_cluster{0};
+  const dim3 threads(32 * S::kWarps);
+  // Short caches and few items: a cluster of CTAs per item, which join their
+  // sums through each other's shared memory: one launch, and no plan to make (1 x
+  // 2064 tokens, 8 KV heads: 6.9 us against 9.0; 16 x 300 to 600: 7.6 against 12.9).
+  // By what the table can hold, the lengths being on the device: as many CTAs as
+  // give every warp one tile, while all clusters run at once (16 clusters of 8,
+  // one too many: 13.0 us against 9.3), and at most two tiles per warp.
+  const int64_t items = (int64_t)a.nseq * a.c.Hkv;
+  const int64_t tiles = (((int64_t)a.width << a.c.log_bs) + kTok - 1) / kTok;
+  int log_c = 0;
+  while ((1 << log_c) < kMaxCluster && tiles > (int64_t)S::kWarps << log_c &&
+         items <= clusters_at_once<D, HEADS>(dev, log_c + 1))
+    ++log_c;
+  if (tiles <= (int64_t)(2 * S::kWarps) << log_c &&
+      items <= clusters_at_once<D, HEADS>(dev, log_c)) {
+    a.cluster = 1 << log_c;
+    return launch_pdl_smem(done_cluster, dev, q4_decode_kernel<D, HEADS, true>,
+                           dim3((unsigned)items << log_c), threads, a.cluster, sizeof(S), st, a);
+  }
+  const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, HEADS, false>, dim3(ctas),
+                                          threads, 1, sizeof(S), st, a);
   if (err != cudaSuccess) return err;
   return launch_pdl(q4_join_kernel<D>, dim3(ctas), dim3(32 * a.G), 0, st, a);
 }
@@ -941,7 +1054,7 @@ cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const
   if (err != cudaSuccess) return err;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   Desc* desc = static_cast<Desc*>(ws);
-  const DecodeArgs a{c, nseq, Hq, Hq / c.Hkv, width, q, table, len, out, lse,
+  const DecodeArgs a{c, nseq, Hq, Hq / c.Hkv, width, 0, q, table, len, out, lse,
                      reinterpret_cast<float*>(desc + kMaxCtas), desc, status,
                      (float)(1.4426950408889634 / std::sqrt((double)c.d))};
   return c.d == 64 ? launch_heads<64>(a, dev, ctas, st) : launch_heads<128>(a, dev, ctas, st);

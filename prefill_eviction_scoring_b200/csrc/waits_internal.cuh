@@ -321,13 +321,15 @@ inline cudaError_t current_sms(int* dev, int* sms) {
   return err;
 }
 
-// launch_pdl for a kernel that needs more than 48 KB of dynamic shared
-// memory.  The opt-in is made once per device (`done`: a bit each); should
-// the launch be refused, because a new context has forgotten it, it is made
-// again.  The opt-in costs about a third of a launch on the host.
+// launch_pdl (in clusters of `cluster` CTAs where that is above 1) for a
+// kernel that needs more than 48 KB of dynamic shared memory.  The opt-in is
+// made once per device (`done`: a bit each); should the launch be refused,
+// because a new context has forgotten it, it is made again.  The opt-in costs
+// about a third of a launch on the host.
 template <typename Kernel, typename... Args>
 cudaError_t launch_pdl_smem(std::atomic<uint64_t>& done, int dev, Kernel kernel, dim3 grid,
-                            dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+                            dim3 block, int cluster, size_t smem, cudaStream_t stream,
+                            Args&&... args) {
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   const bool fresh = !(done.load(std::memory_order_relaxed) & bit);
   for (int tries = fresh ? 1 : 2;; --tries) {
@@ -337,7 +339,9 @@ cudaError_t launch_pdl_smem(std::atomic<uint64_t>& done, int dev, Kernel kernel,
       if (err != cudaSuccess) return err;
       done.fetch_or(bit, std::memory_order_relaxed);
     }
-    const cudaError_t err = launch_pdl(kernel, grid, block, smem, stream, args...);
+    const cudaError_t err =
+        cluster > 1 ? launch_pdl_cluster(kernel, grid, block, cluster, smem, stream, args...)
+                    : launch_pdl(kernel, grid, block, smem, stream, args...);
     if (err != cudaErrorInvalidValue || tries == 1) return err;
     cudaGetLastError();
   }

@@ -926,3 +926,26 @@ def test_empty_calls():
     api.q4_append(none, none, slots, pool)
     K, V = api.q4_read(pool, slots, 64)
     assert K.shape == V.shape == (0, 2, 64) and torch.equal(pool, before)
+
+
+@pytest.mark.parametrize("nseq,Hq,Hkv,d,hi", [
+    (1, 32, 8, 128, 2500), (1, 16, 1, 128, 40), (2, 28, 4, 128, 3000), (3, 8, 2, 64, 6000),
+    (7, 16, 8, 64, 700), (16, 16, 4, 128, 380), (60, 4, 2, 128, 700), (140, 3, 1, 64, 300)])
+def test_attend_short_and_wide_tables(nseq, Hq, Hkv, d, hi):
+    """A table that holds little has clusters of 1, 2, 4 or 8 CTAs per item,
+    some without a tile of their own; a wide one of the same contents does
+    not.  Both agree with the oracle."""
+    rng = np.random.default_rng(hi)
+    lens = rng.integers(0, hi + 1, nseq).tolist()
+    lens[0] = hi
+    if nseq > 2:
+        lens[1], lens[2] = 0, 33
+    g = _gen(hi + nseq)
+    pool, table, kv = _fill(g, lens, Hkv, d, 16)
+    q = _bf(g, nseq, Hq, d)
+    wide = torch.full((nseq, 20000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    for t in (table, wide):
+        a = _check_attend(q, pool, t, lens, kv)
+        b = api.q4_decode_attention(q, pool, t, _i32(lens), True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
