@@ -5,8 +5,8 @@
 // free stack are its own, a prefix sum of the new tokens where its slots
 // start.  Latency bounds it: a decode step moves a few hundred bytes.  So one
 // launch does all of it, of one CTA for up to 4096 slots (64 sequences, one
-// token each: 4.9 us on the GPU, against 6.1 with a cluster) and of a cluster
-// of 8 for more (8 prompts, 131072 slots, 0.5 MB: 8.9 us): every CTA repeats
+// token each: 4.7 us on the GPU, against 6.1 with a cluster) and of a cluster
+// of 8 for more (8 prompts, 131072 slots, 0.5 MB: 8.9 us, instructions): every CTA repeats
 // the (cheap) prefix sums in its shared memory and writes its share of the
 // slots, and after a barrier, when nobody reads the old lengths any more, the
 // first one updates lengths and count in place.  A thread makes four
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kCtas = 8;
+constexpr int kGroups = 4;         // groups of four slots that a thread makes at a time
 
 // Inclusive prefix sum over the block's threads; `sums` is shared memory that
 // no thread still reads (two calls in a row take two).
@@ -102,56 +103,76 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
       total[1] = upto;
     }
   }
-  // slots, four neighbouring tokens per thread and step: their block is
-  // looked up once, or where it changes
+  // slots: groups of four neighbouring tokens, kGroups of them per thread at a
+  // time so that their block look-ups are in flight together
   const int ntok = cu[a.nseq] < a.max_new ? cu[a.nseq] : a.max_new;
   const bool vec = a.slots && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
-#pragma unroll 2
-  for (int64_t i0 = (int64_t)(rank * kThreads + t) * 4; i0 < a.max_new;
-       i0 += (int64_t)ranks * kThreads * 4) {
-    int slot[4] = {-1, -1, -1, -1};
-    if (i0 < ntok) {
-      int lo = 0, hi = a.nseq;           // the last s with cu[s] <= i0
+  auto block_of = [&](int s, int pos) {  // looks the block up; fills in the table
+    const int logical = pos >> a.log_bs, have = (int)(((int64_t)held[s] + bs1) >> a.log_bs);
+    int32_t* entry = a.table + (int64_t)s * a.width + logical;
+    if (logical < have) return *entry;
+    return __ldg(a.free_list + (free_n - 1 - (first[s] + logical - have)));
+  };
+  auto enter = [&](int s, int pos, int block) {
+    // the first token of a block is always a new one, and so is the block
+    if ((pos & bs1) == 0) a.table[(int64_t)s * a.width + (pos >> a.log_bs)] = block;
+  };
+  auto slot_of = [&](int pos, int block) {
+    if ((unsigned)block < (unsigned)a.num_blocks) return (block << a.log_bs) + (pos & bs1);
+    bits |= WAITS_DEV_BAD_INDEX;
+    return -1;
+  };
+  const int64_t stride = (int64_t)ranks * kThreads * 4;
+  for (int64_t base = (int64_t)(rank * kThreads + t) * 4; base < a.max_new;
+       base += stride * kGroups) {
+    int s[kGroups], pos[kGroups], block[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int64_t i0 = base + k * stride;
+      s[k] = pos[k] = block[k] = -1;
+      if (i0 >= ntok) continue;
+      int lo = 0, hi = a.nseq;           // the last sequence with cu[s] <= i0
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cu[mid] <= i0) lo = mid; else hi = mid;
       }
-      int s = lo, block = -1;
-      bool fresh = true;                 // the block is not known yet
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = i0 + e;
-        if (i >= ntok) break;
-        while (cu[s + 1] <= i) {
-          ++s;
-          fresh = true;
-        }
-        if (first[s] < 0) continue;
-        const int len = held[s];
-        const int pos = len + (int)(i - cu[s]);
-        if (fresh || (pos & bs1) == 0) {
-          const int logical = pos >> a.log_bs;
-          const int have = (int)(((int64_t)len + bs1) >> a.log_bs);
-          int32_t* entry = a.table + (int64_t)s * a.width + logical;
-          if (logical < have) {
-            block = *entry;
-          } else {
-            block = __ldg(a.free_list + (free_n - 1 - (first[s] + logical - have)));
-            // the first token of a block is always a new one
-            if ((pos & bs1) == 0) *entry = block;
-          }
-          fresh = false;
-        }
-        if ((unsigned)block < (unsigned)a.num_blocks)
-          slot[e] = (block << a.log_bs) + (pos & bs1);
-        else
-          bits |= WAITS_DEV_BAD_INDEX;
-      }
+      s[k] = lo;
+      if (first[lo] < 0) continue;
+      pos[k] = held[lo] + (int)(i0 - cu[lo]);
+      block[k] = block_of(lo, pos[k]);
     }
-    if (vec && i0 + 4 <= a.max_new)
-      *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-    else if (a.slots)
-      for (int e = 0; e < 4 && i0 + e < a.max_new; ++e) a.slots[i0 + e] = slot[e];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int64_t i0 = base + k * stride;
+      if (i0 >= a.max_new) break;
+      int slot[4] = {-1, -1, -1, -1};
+      if (s[k] >= 0) {
+        int q = s[k], at = pos[k], b = block[k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t i = i0 + e;
+          if (i >= ntok) break;
+          if (e > 0) {
+            bool other = false;          // another sequence, or another block of this one
+            while (cu[q + 1] <= i) {
+              ++q;
+              other = true;
+            }
+            if (first[q] < 0) continue;
+            at = held[q] + (int)(i - cu[q]);
+            if (other || (at & bs1) == 0) b = block_of(q, at);
+          } else if (at < 0) {
+            continue;
+          }
+          enter(q, at, b);
+          slot[e] = slot_of(at, b);
+        }
+      }
+      if (vec && i0 + 4 <= a.max_new)
+        *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      else if (a.slots)
+        for (int e = 0; e < 4 && i0 + e < a.max_new; ++e) a.slots[i0 + e] = slot[e];
+    }
   }
   if (a.status && bits) atomicOr(a.status, bits);
   if (CLUSTER)
