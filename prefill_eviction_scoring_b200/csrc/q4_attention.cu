@@ -327,7 +327,17 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
                        total * items < (int64_t)kEndTiles * grid * (grid - items);
     int per = 1;                           // CTAs per item of this lane's sequence
     if (apart) {
-      const int most = max((int)((total + grid - items - 1) / (grid - items)), kMinTiles);
+      // runs of total / (grid - items) tiles never need more CTAs than there
+      // are; where the lengths differ, the shortest runs that do not are searched
+      int most = max((int)((total + grid - items - 1) / (grid - items)), kMinTiles);
+      if (__any_sync(0xffffffffu, mine > 0 && (int64_t)mine * items != total)) {
+        int low = max((int)((total + grid - 1) / grid), kMinTiles);
+        while (low < most) {
+          const int mid = (low + most) / 2;
+          if (__reduce_add_sync(0xffffffffu, (mine + mid - 1) / mid) * Hkv <= grid) most = mid;
+          else low = mid + 1;
+        }
+      }
       per = (mine + most - 1) / most;
     }
     ctas = stream_ctas(total, grid);
