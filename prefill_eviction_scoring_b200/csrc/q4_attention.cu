@@ -50,7 +50,6 @@ namespace {
 
 constexpr int kJoiners = 4;           // warps that add up an item's sums, in turn
 constexpr int kSub = 16;              // tokens of one mma step; a page is a multiple of it
-constexpr int kTok = 2 * kSub;        // tokens per tile
 constexpr int kStages = 2;
 constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 9.9 us for 9.0 on 1 x 2064
                                       // without a cluster)
@@ -165,20 +164,26 @@ __device__ inline float max4(float a, float b, float c, float d) {
 // Twelve warps at 168 registers; the sums of 16 heads of 128 dimensions need
 // more, and eight warps have them (69 us with twelve, which spill, 56
 // with eight: 64 sequences of 16384 tokens, 16 heads on one).
-template <int D, int HEADS>
+template <int D, int HEADS, bool CLUSTER>
 struct Smem {
   static constexpr int kWarps = D == 128 && HEADS == 16 ? 8 : 12;
+  // A tile's parts of 16 tokens: 2, or 4 where the registers allow it, which
+  // halves the work per tile that is not per token (32 sequences of 16384
+  // tokens, d = 64: 77.7 us with 2, 68.1 with 4); short caches want every warp
+  // to have a tile (1 x 2064: 5.7 with 2, 6.3 with 4).
+  static constexpr int kParts = D == 64 && HEADS <= 8 && !CLUSTER ? 4 : 2;
+  static constexpr int kTok = kParts * kSub;
   static constexpr int kCodes = kSub * D / 2;           // bytes of a half tile's K (or V) codes
   static constexpr int kScales = kSub * D / 16;
   static constexpr int kHalf = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
-  static constexpr int kTileBytes = 2 * kHalf;
+  static constexpr int kTileBytes = kParts * kHalf;
   static constexpr int kRow = D + 4;                    // floats per merge row, no bank conflicts
   uint8_t ring[kWarps][kStages][kTileBytes];
   static constexpr int kSlots = HEADS == 16 ? 1 : 2;    // items whose ends may overlap
   float o[kSlots][kWarps][HEADS][kRow];
   float m[kSlots][kWarps][HEADS], l[kSlots][kWarps][HEADS];
   uint64_t full[kSlots], free[kSlots];
-  int32_t page_ok[kWarps][kStages][2];
+  int32_t page_ok[kWarps][kStages][kParts];
   float all_o[HEADS][D], all_m[HEADS], all_l[HEADS];    // the CTA's sums, for its cluster
   int64_t scan[kWarps];
   int64_t where[2];                                     // sequence of the run's start, units before it
@@ -254,12 +259,13 @@ __device__ inline int cta_of(int64_t unit, int64_t total, int ctas) {
 // use the columns twice: 0 - 3 weigh with V's scale of the even group, 4 - 7
 // with the odd group's.
 template <int D, int HEADS, bool CLUSTER>
-__global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
+__global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     q4_decode_kernel(const DecodeArgs a) {
   constexpr int NG = D / 32, NW2 = D / 64, NT = HEADS == 16 ? 2 : 1;
   constexpr bool kTwice = HEADS == 4;
-  using S = Smem<D, HEADS>;
+  using S = Smem<D, HEADS, CLUSTER>;
   constexpr int kWarps = S::kWarps, kThreads = 32 * kWarps;
+  constexpr int kParts = S::kParts, kTok = S::kTok;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -434,7 +440,8 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
   // copies a half tile, whose page it looks up one tile ahead.
   int p_left = 0;                          // tiles not yet issued
   if (run > warp) p_left = (int)((run - warp + kWarps - 1) / kWarps);
-  int p_s = s, p_g = g, p_n = tokens(s), p_nt = nt, p_tile = tile0, p_stage = 0, p_block = -1;
+  int p_s = s, p_g = g, p_n = tokens(s), p_nt = nt, p_tile = tile0, p_stage = 0;
+  int p_block[kParts / 2];                 // of the half's parts: half, half + 2, ..
   const int32_t* p_row = a.table + (int64_t)s * a.width;
   const int half = lane >> 4, hl = lane & 15;
   auto settle = [&]() {                    // bring p_tile into its item; load the half's block
@@ -449,8 +456,11 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
       } while (p_tile >= p_nt);
       p_row = a.table + (int64_t)p_s * a.width;
     }
-    const int j = p_tile * kTok + half * kSub;   // a tile's second half may lie past the end
-    p_block = j < p_n ? __ldg(p_row + (j >> log_bs)) : -2;
+#pragma unroll
+    for (int h = 0; h < kParts / 2; ++h) { // a tile's later parts may lie past the end
+      const int j = p_tile * kTok + (half + 2 * h) * kSub;
+      p_block[h] = j < p_n ? __ldg(p_row + (j >> log_bs)) : -2;
+    }
   };
   if (p_left > 0) {
     p_tile += warp;
@@ -474,22 +484,26 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
   const uint32_t sc_dst = 2 * S::kCodes + sc_which * S::kScales + sc_ch * 16;
   auto issue = [&]() {
     if (p_left > 0) {
-      const bool ok = (unsigned)p_block < (unsigned)a.c.num_blocks;
-      if (hl == 0) sm.page_ok[warp][p_stage][half] = ok;
-      if (ok) {
-        const uint32_t off = (p_tile * kTok + half * kSub) & ((1 << log_bs) - 1);
-        const uint8_t* page = pool + (uint32_t)p_block * block_bytes + p_g * (uint32_t)page_bytes;
-        const uint8_t* kc = page + off * (D / 2);
-        const uint8_t* vc = kc + v_range;
-        const uint32_t dst = ring + p_stage * S::kTileBytes;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {             // rows 16 / NG further each
-          cp_async16(dst + k_dst + i * 256, kc + i * 256);
-          cp_async16(dst + (D == 128 && i >= 2 ? v_dst ^ 32 : v_dst) + i * 64, vc + i * 256);
+      for (int h = 0; h < kParts / 2; ++h) {
+        const bool ok = (unsigned)p_block[h] < (unsigned)a.c.num_blocks;
+        if (hl == 0) sm.page_ok[warp][p_stage][half + 2 * h] = ok;
+        if (ok) {
+          const uint32_t off = (p_tile * kTok + (half + 2 * h) * kSub) & ((1 << log_bs) - 1);
+          const uint8_t* page =
+              pool + (uint32_t)p_block[h] * block_bytes + p_g * (uint32_t)page_bytes;
+          const uint8_t* kc = page + off * (D / 2);
+          const uint8_t* vc = kc + v_range;
+          const uint32_t dst = ring + p_stage * S::kTileBytes + 2 * h * S::kHalf;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {           // rows 16 / NG further each
+            cp_async16(dst + k_dst + i * 256, kc + i * 256);
+            cp_async16(dst + (D == 128 && i >= 2 ? v_dst ^ 32 : v_dst) + i * 64, vc + i * 256);
+          }
+          if (D == 128 || hl < D / 8) cp_async16(dst + sc_dst, page + sc_src + off * (D / 16));
+        } else if (a.status && p_block[h] != -2 && hl == 0) {
+          atomicOr(a.status, WAITS_DEV_BAD_INDEX);
         }
-        if (D == 128 || hl < D / 8) cp_async16(dst + sc_dst, page + sc_src + off * (D / 16));
-      } else if (a.status && p_block != -2 && hl == 0) {
-        atomicOr(a.status, WAITS_DEV_BAD_INDEX);
       }
       p_stage = p_stage + 1 == kStages ? 0 : p_stage + 1;
       if (--p_left > 0) {
@@ -559,14 +573,22 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
       issue();
       const uint8_t* st = &sm.ring[warp][stage][0];
       const int valid = n - (k - base) * kTok;
-      const int2 ok = *reinterpret_cast<const int2*>(&sm.page_ok[warp][stage][0]);
+      int ok[kParts];
+#pragma unroll
+      for (int h = 0; h < kParts; h += 2) {
+        const int2 x = *reinterpret_cast<const int2*>(&sm.page_ok[warp][stage][h]);
+        ok[h] = x.x;
+        ok[h + 1] = x.y;
+      }
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      const bool edge = valid < kTok || !ok.x || !ok.y;
+      bool edge = valid < kTok;
+#pragma unroll
+      for (int h = 0; h < kParts; ++h) edge |= !ok[h];
       // this lane's tokens: rows r and r + 8 of the first product
       const int p0 = 4 * (r >> 1) + (r & 1), p1 = p0 + 2;
-      float lg[NT][2][2][2];                           // [half][token][head]
+      float lg[NT][kParts][2][2];                      // [part][token][head]
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < kParts; ++hf) {
         const uint8_t* sh = st + hf * S::kHalf;
         uint32_t k0w[NG], k1w[NG], s0[NW2], s1[NW2];
         if (D == 128) {
@@ -613,16 +635,23 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
       // no page), a maximum that lags by more than 2^kSlack, scales of V that
       // outgrow their unit.
       bool rare = edge;
+      auto most = [&](int t, int b) {
+        float x = max4(lg[t][0][0][b], lg[t][0][1][b], lg[t][1][0][b], lg[t][1][1][b]);
+        if (kParts == 4)
+          x = fmaxf(x, max4(lg[t][kParts - 2][0][b], lg[t][kParts - 2][1][b],
+                            lg[t][kParts - 1][0][b], lg[t][kParts - 1][1][b]));
+        return x;
+      };
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float2 qs = unpair(qscale[t]);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          rare |= max4(lg[t][0][0][b], lg[t][0][1][b], lg[t][1][0][b], lg[t][1][1][b]) *
-                      (b ? qs.y : qs.x) > m[t][b] + kSlack;
+          rare |= most(t, b) * (b ? qs.y : qs.x) > m[t][b] + kSlack;
       }
-      {                                                // lane: the scales of one token
-        const uint8_t* at = st + half * S::kHalf + 2 * S::kCodes + S::kScales + hl * (D / 16);
+#pragma unroll
+      for (int h = 0; h < kParts; h += 2) {            // lane: the scales of one token of two parts
+        const uint8_t* at = st + (half + h) * S::kHalf + 2 * S::kCodes + S::kScales + hl * (D / 16);
         if (D == 128) {
           const uint2 x = *reinterpret_cast<const uint2*>(at);
           rare |= __vmaxu2(x.x, limit[0]) != limit[0] ||
@@ -632,22 +661,25 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
         }
       }
       if (__any_sync(0xffffffffu, rare)) {
-        uint32_t* own = reinterpret_cast<uint32_t*>(
-            const_cast<uint8_t*>(st) + half * S::kHalf + 2 * S::kCodes + S::kScales +
-            hl * (D / 16));
+        // V's scales of this lane's token of parts h, h + 1
+        auto own = [&](int h) {
+          return reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(st) + (half + h) * S::kHalf +
+                                             2 * S::kCodes + S::kScales + hl * (D / 16));
+        };
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (16 * (i / 2) + (i % 2 ? p1 : p0) >= valid || !(i < 2 ? ok.x : ok.y)) {
+          for (int i = 0; i < 2 * kParts; ++i)
+            if (16 * (i / 2) + (i % 2 ? p1 : p0) >= valid || !ok[i / 2]) {
 #pragma unroll
               for (int t = 0; t < NT; ++t)
                 lg[t][i / 2][i % 2][0] = lg[t][i / 2][i % 2][1] = -INFINITY;
             }
-          // no weight: zero scales (lane: one token)
-          if (lane >= valid || !(lane < kSub ? ok.x : ok.y)) {
 #pragma unroll
-            for (int i = 0; i < NW2; ++i) own[i] = 0;
-          }
+          for (int h = 0; h < kParts; h += 2)          // no weight: zero scales
+            if (h * kSub + lane >= valid || !(lane < kSub ? ok[h] : ok[h + 1])) {
+#pragma unroll
+              for (int i = 0; i < NW2; ++i) own(h)[i] = 0;
+            }
           __syncwarp();
         }
 #pragma unroll
@@ -656,8 +688,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
           float f[2];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            float top = max4(lg[t][0][0][b], lg[t][0][1][b], lg[t][1][0][b], lg[t][1][1][b]) *
-                        (b ? qs.y : qs.x);
+            float top = most(t, b) * (b ? qs.y : qs.x);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -674,8 +705,12 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           const int sft = 16 * (gr % 2);
-          uint32_t x = (own[gr / 2] >> sft) & 0xffffu;
-          x = x < 0x7f80u ? x : 0;
+          uint32_t x = 0;
+#pragma unroll
+          for (int h = 0; h < kParts; h += 2) {
+            const uint32_t y = (own(h)[gr / 2] >> sft) & 0xffffu;
+            x = y < 0x7f80u ? max(x, y) : x;
+          }
           x = __reduce_max_sync(0xffffffffu, x);
           const uint32_t mask = 0xffffu << sft;
           const uint32_t was = (unit[gr / 2] >> sft) & 0xffffu;
@@ -699,7 +734,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
         const uint64_t ref = pair(m[t][0] == -INFINITY ? 0.f : -m[t][0],
                                   m[t][1] == -INFINITY ? 0.f : -m[t][1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kParts; ++i) {
           float(&x)[2] = lg[t][i / 2][i % 2];
           const float2 y = unpair(fma2(pair(x[0], x[1]), qscale[t], ref));
           x[0] = ex2(y.x);
@@ -709,7 +744,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS>::kWarps, 1)
       }
       // O^T[d, head] += V^T[d, token] (p scale)[token, head], group by group
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < kParts; ++hf) {
         const uint8_t* sh = st + hf * S::kHalf;
         const uint8_t* sc = sh + 2 * S::kCodes + S::kScales;
         uint32_t s0[NW2], s1[NW2], vw[4][NW2];
@@ -992,7 +1027,7 @@ int clusters_at_once(int dev, int log_c) {
   if (dev >= 64) return 0;
   int n = known[dev][log_c].load(std::memory_order_relaxed) - 1;
   if (n >= 0) return n;
-  using S = Smem<D, HEADS>;
+  using S = Smem<D, HEADS, true>;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(1 << log_c);
   cfg.blockDim = dim3(32 * S::kWarps);
@@ -1016,7 +1051,8 @@ int clusters_at_once(int dev, int log_c) {
 
 template <int D, int HEADS>
 cudaError_t launch_d(DecodeArgs a, int dev, int ctas, cudaStream_t st) {
-  using S = Smem<D, HEADS>;
+  using S = Smem<D, HEADS, true>;
+  using Long = Smem<D, HEADS, false>;
   static std::atomic<uint64_t> done{0}, done_cluster{0};
   const dim3 threads(32 * S::kWarps);
   // Short caches and few items: a cluster of CTAs per item, which join their
@@ -1026,7 +1062,7 @@ cudaError_t launch_d(DecodeArgs a, int dev, int ctas, cudaStream_t st) {
   // give every warp one tile, while all clusters run at once (16 clusters of 8,
   // one too many: 13.0 us against 9.3), and at most two tiles per warp.
   const int64_t items = (int64_t)a.nseq * a.c.Hkv;
-  const int64_t tiles = (((int64_t)a.width << a.c.log_bs) + kTok - 1) / kTok;
+  const int64_t tiles = (((int64_t)a.width << a.c.log_bs) + S::kTok - 1) / S::kTok;
   int log_c = 0;
   while ((1 << log_c) < kMaxCluster && tiles > (int64_t)S::kWarps << log_c &&
          items <= clusters_at_once<D, HEADS>(dev, log_c + 1))
@@ -1038,7 +1074,7 @@ cudaError_t launch_d(DecodeArgs a, int dev, int ctas, cudaStream_t st) {
                            dim3((unsigned)items << log_c), threads, a.cluster, sizeof(S), st, a);
   }
   const cudaError_t err = launch_pdl_smem(done, dev, q4_decode_kernel<D, HEADS, false>, dim3(ctas),
-                                          threads, 1, sizeof(S), st, a);
+                                          dim3(32 * Long::kWarps), 1, sizeof(Long), st, a);
   if (err != cudaSuccess) return err;
   return launch_pdl(q4_join_kernel<D>, dim3(ctas), dim3(32 * a.G), 0, st, a);
 }
@@ -1071,3 +1107,4 @@ cudaError_t launch_q4_decode(const Q4Pool& c, int nseq, int Hq, int width, const
 }
 
 }  // namespace waits
+
