@@ -161,17 +161,18 @@ __device__ inline float max4(float a, float b, float c, float d) {
 }
 
 // HEADS: query heads of a group that the kernel is built for, 4, 8 or 16.
-// Twelve warps at 168 registers; the sums of 16 heads of 128 dimensions need
-// more, and eight warps have them (69 us with twelve, which spill, 56
-// with eight: 64 sequences of 16384 tokens, 16 heads on one).
+// CLUSTER: an item's CTAs are a cluster (short caches).
 template <int D, int HEADS, bool CLUSTER>
 struct Smem {
-  static constexpr int kWarps = D == 128 && HEADS == 16 ? 8 : 12;
-  // A tile's parts of 16 tokens: 2, or 4 where the registers allow it, which
-  // halves the work per tile that is not per token (32 sequences of 16384
-  // tokens, d = 64: 77.7 us with 2, 68.1 with 4); short caches want every warp
-  // to have a tile (1 x 2064: 5.7 with 2, 6.3 with 4).
-  static constexpr int kParts = D == 64 && HEADS <= 8 && !CLUSTER ? 4 : 2;
+  // A tile's parts of 16 tokens.  4 halve the work per tile that is not per
+  // token and let a warp run four products at once, but want more registers
+  // than 12 warps have at d = 128: 8 warps of 255 then (32 sequences of 16384
+  // tokens: 114.0 us with 12 warps and 2 parts, 109.7 with 8 and 4; d = 64, 12
+  // warps: 77.7 and 68.0).  Short caches want every warp to have a tile: 2
+  // parts (1 x 2064, d = 64: 5.7 us against 6.3).  The sums of 16 heads leave no
+  // room for more than 2 (and at d = 128 for more than 8 warps).
+  static constexpr int kParts = HEADS <= 8 && !CLUSTER ? 4 : 2;
+  static constexpr int kWarps = D == 128 && (HEADS == 16 || !CLUSTER) ? 8 : 12;
   static constexpr int kTok = kParts * kSub;
   static constexpr int kCodes = kSub * D / 2;           // bytes of a half tile's K (or V) codes
   static constexpr int kScales = kSub * D / 16;
