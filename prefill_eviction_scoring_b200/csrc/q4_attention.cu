@@ -54,9 +54,9 @@ constexpr int kStages = 2;
 constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 9.9 us for 9.0 on 1 x 2064
                                       // without a cluster)
 // What the end of an item inside a run may cost, in tiles of the run: measured
-// at 20, 60 and 100 on 8 sequences of 4096 tokens (17.6, 16.6, 16.6 us), of 2064
-// (14.8, 12.5, 12.5) and of 1000 to 16384 (33.9, 33.9, 37.3).
-constexpr int kEndTiles = 60;
+// at 30 and 60 on 8 sequences of 1000 to 16384 tokens (31.4, 33.0 us) and of 4096
+// (15.5 both), and at 10 (in tiles of 64) on the latter (17.6).
+constexpr int kEndTiles = 30;
 constexpr int kMaxCluster = 8;        // CTAs of an item's cluster
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
