@@ -57,6 +57,7 @@ constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 
 // at 30 and 60 on 8 sequences of 1000 to 16384 tokens (31.4, 33.0 us) and of 4096
 // (15.5 both), and at 10 (in tiles of 64) on the latter (17.6).
 constexpr int kEndTiles = 30;
+constexpr int kSoloTiles = 8;         // tiles per item on average, up to which a warp takes it alone
 constexpr int kMaxCluster = 8;        // CTAs of an item's cluster
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
@@ -303,10 +304,12 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
         for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)s * a.Hq + i] = -INFINITY;
     }
   };
-  // This CTA's run: `run` tiles from tile0 of item (s, g) on, which has nt.
+  // This CTA's run: `run` tiles from tile0 of item (s, g) on, which has nt; or,
+  // where items are many and short, `run` items from (s, g) on, one warp each.
   int s, g, tile0, nt;
   int64_t run, total = 0, u0 = 0;          // u0: tiles before the run
   int ctas = 0, parts = 0;                 // parts: CTAs per item, 0 where runs cross items
+  bool solo = false;
   const int grid = gridDim.x, me = blockIdx.x;
   const int mine_of = CLUSTER ? me % a.cluster : 0;   // this CTA's place among its item's
   if (CLUSTER) {
@@ -330,6 +333,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     total = warp_sum((int64_t)mine) * Hkv;
     // Whole CTAs per item, where that lengthens the longest run by less than
     // the end of an item inside a run costs.
+    solo = items > 2 * grid && total <= (int64_t)kSoloTiles * items;
     const bool apart = total > 0 && 2 * items <= grid &&
                        total * items < (int64_t)kEndTiles * grid * (grid - items);
     int per = 1;                           // CTAs per item of this lane's sequence
@@ -347,9 +351,10 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
       }
       per = (mine + most - 1) / most;
     }
-    ctas = stream_ctas(total, grid);
-    u0 = apart || me >= ctas ? me : split(total, me, ctas);
-    const int64_t x = (int64_t)(apart ? per : mine) * Hkv;
+    const int64_t units = solo ? items : total;
+    ctas = solo ? grid : stream_ctas(total, grid);
+    u0 = apart || me >= ctas ? me : split(units, me, ctas);
+    const int64_t x = (int64_t)(apart ? per : solo ? mine > 0 : mine) * Hkv;
     int64_t upto = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -371,29 +376,39 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
       tile0 = (int)split(nt, i, parts);
       run = split(nt, i + 1, parts) - tile0;
     } else {
-      g = in_seq >> 32 ? (int)(in_seq / nt) : (int)((uint32_t)in_seq / (uint32_t)nt);
-      tile0 = (int)(in_seq - (int64_t)g * nt);
-      run = split(total, me + 1, ctas) - u0;
+      run = split(units, me + 1, ctas) - u0;
+      g = solo           ? (int)in_seq
+          : in_seq >> 32 ? (int)(in_seq / nt)
+                         : (int)((uint32_t)in_seq / (uint32_t)nt);
+      tile0 = solo ? 0 : (int)(in_seq - (int64_t)g * nt);
     }
   } else {
     int64_t mine = 0;
-    for (int i = tid; i < a.nseq; i += kThreads) mine += tiles(i);
+    // tiles, and from bit 40 on the sequences that have any
+    for (int i = tid; i < a.nseq; i += kThreads) {
+      const int n = tiles(i);
+      mine += n + ((int64_t)(n > 0) << 40);
+    }
     mine = warp_sum(mine);
     if (lane == 0) sm.scan[warp] = mine;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
-    total *= Hkv;
-    ctas = stream_ctas(total, grid);
+    const int64_t items = (total >> 40) * Hkv;
+    total = (total & (((int64_t)1 << 40) - 1)) * Hkv;
+    solo = items > 2 * grid && total <= kSoloTiles * items;
+    const int64_t units = solo ? items : total;
+    ctas = solo ? grid : stream_ctas(total, grid);
     if (me >= ctas) {
       zero_empty();
       return;
     }
-    u0 = split(total, me, ctas);
-    run = split(total, me + 1, ctas) - u0;
+    u0 = split(units, me, ctas);
+    run = split(units, me + 1, ctas) - u0;
     // the sequence of u0: prefix sums, kThreads sequences at a time
     int64_t before = 0;
     for (int s0 = 0; before <= u0; s0 += kThreads) {
-      const int64_t x = s0 + tid < a.nseq ? (int64_t)tiles(s0 + tid) * Hkv : 0;
+      const int in = s0 + tid < a.nseq ? tiles(s0 + tid) : 0;
+      const int64_t x = (int64_t)(solo ? in > 0 : in) * Hkv;
       int64_t upto = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -418,9 +433,19 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     __syncthreads();
     s = (int)sm.where[0];
     nt = tiles(s);
-    g = (int)(sm.where[1] / nt);
-    tile0 = (int)(sm.where[1] - (int64_t)g * nt);
+    g = (int)(solo ? sm.where[1] : sm.where[1] / nt);
+    tile0 = solo ? 0 : (int)(sm.where[1] - (int64_t)g * nt);
   }
+  // Moves (s, g) `by` items on, past empty sequences.
+  auto advance = [&](int& s, int& g, int& nt, int by) {
+    for (g += by; g >= Hkv; g -= Hkv) {
+      do ++s; while ((nt = tiles(s)) == 0);
+    }
+  };
+  // how many tiles further a warp's next one is; solo: this warp's items
+  const int step = solo ? 1 : kWarps;
+  const int my_items = solo && run > warp ? ((int)run - warp + kWarps - 1) / kWarps : 0;
+  if (my_items > 0) advance(s, g, nt, warp);
   // Q's fragments: column r is head r (and r + 8), dimensions 16 k + 4 c .. + 3
   uint2 raw[NT][D / 16];
   auto load_q = [&](int s, int g) {
@@ -440,21 +465,26 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
   // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..  A half warp
   // copies a half tile, whose page it looks up one tile ahead.
   int p_left = 0;                          // tiles not yet issued
-  if (run > warp) p_left = (int)((run - warp + kWarps - 1) / kWarps);
+  if (solo)
+    p_left = my_items > 0 ? 0x7fffffff : 0;            // until the items have run out
+  else if (run > warp)
+    p_left = (int)((run - warp + kWarps - 1) / kWarps);
+  int p_items = my_items;
   int p_s = s, p_g = g, p_n = tokens(s), p_nt = nt, p_tile = tile0, p_stage = 0;
   int p_block[kParts / 2];                 // of the half's parts: half, half + 2, ..
   const int32_t* p_row = a.table + (int64_t)s * a.width;
   const int half = lane >> 4, hl = lane & 15;
   auto settle = [&]() {                    // bring p_tile into its item; load the half's block
     if (p_tile >= p_nt) {
+      if (solo && --p_items == 0) {
+        p_left = 0;
+        return;
+      }
       do {
         p_tile -= p_nt;
-        if (++p_g == Hkv) {
-          p_g = 0;
-          do ++p_s; while ((p_n = tokens(p_s)) == 0);
-          p_nt = (int)(((int64_t)p_n + kTok - 1) / kTok);
-        }
+        advance(p_s, p_g, p_nt, solo ? kWarps : 1);
       } while (p_tile >= p_nt);
+      p_n = tokens(p_s);
       p_row = a.table + (int64_t)p_s * a.width;
     }
 #pragma unroll
@@ -464,7 +494,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     }
   };
   if (p_left > 0) {
-    p_tile += warp;
+    if (!solo) p_tile += warp;
     settle();
   }
   // Where a lane's 16-byte pieces hl, hl + 16, .. of a half come from and go:
@@ -508,13 +538,13 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
       }
       p_stage = p_stage + 1 == kStages ? 0 : p_stage + 1;
       if (--p_left > 0) {
-        p_tile += kWarps;
+        p_tile += step;
         settle();
       }
     }
     cp_async_commit();
   };
-  if (!CLUSTER || run > 0) load_q(s, g);
+  if (solo ? my_items > 0 : !CLUSTER || run > 0) load_q(s, g);
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) issue();
   if (!CLUSTER) zero_empty();
@@ -523,9 +553,9 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
   int stage = 0, item = 0;
   bool first = true;
   const int run_tiles = (int)run;
-  for (int u = 0; u < run_tiles;) {
+  for (int u = 0; solo ? item < my_items : u < run_tiles;) {
     const int n = tokens(s);
-    const int piece = min(run_tiles - u, nt - tile0);
+    const int piece = solo ? nt : min(run_tiles - u, nt - tile0);
     uint32_t qf[NT][D / 16][2];
     uint64_t qscale[NT];                               // of heads 2 c, 2 c + 1
 #pragma unroll
@@ -567,8 +597,8 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     }
     int k0 = u;                                        // first tile of this warp in the piece
     const int kend = u + piece, base = u - tile0;
-    k0 += (warp + kWarps - k0 % kWarps) % kWarps;
-    for (int k = k0; k < kend; k += kWarps) {
+    if (!solo) k0 += (warp + kWarps - k0 % kWarps) % kWarps;
+    for (int k = k0; k < kend; k += step) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
       issue();
@@ -815,12 +845,48 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     }
     // ---- the item's end: join the warps' sums, the next item's queries on the way
     int next_s = s, next_g = g, next_nt = nt;
-    if (u + piece < run_tiles) {
-      if (++next_g == Hkv) {
-        next_g = 0;
-        do ++next_s; while ((next_nt = tiles(next_s)) == 0);
-      }
+    if (solo ? item + 1 < my_items : u + piece < run_tiles) {
+      advance(next_s, next_g, next_nt, solo ? kWarps : 1);
       load_q(next_s, next_g);
+    }
+    if (solo) {                                        // the warp's sums are the item's
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float2 l = unpair(l2[t]);
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l.x += __shfl_xor_sync(0xffffffffu, l.x, x);
+          l.y += __shfl_xor_sync(0xffffffffu, l.y, x);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int h = 2 * (kTwice ? c & 1 : c) + b + 8 * t;
+          if (h >= G) continue;
+          const float L = b ? l.y : l.x, inv = L == 0.f ? 0.f : 1.f / L;
+          const size_t row = (size_t)s * a.Hq + (size_t)g * G + h;
+#pragma unroll
+          for (int gr = 0; gr < NG; gr += kTwice ? 2 : 1) {
+            const bool odd = kTwice && c >= 2;         // this column's group
+            const uint32_t un =
+                (unit[gr / 2] >> (kTwice ? (odd ? 23 : 7) : 16 * (gr % 2) + 7)) & 0xffu;
+            const float v = __uint_as_float((254 - un) << 23);
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              x[i] = (odd ? o[t][kTwice ? gr + 1 : gr][i / 2][2 * (i % 2) + b]
+                          : o[t][gr][i / 2][2 * (i % 2) + b]) * inv * v;
+            *reinterpret_cast<uint2*>(a.out + row * D + 32 * (gr + odd) + 4 * r) =
+                make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+          }
+          if (a.lse && r == 0 && (!kTwice || c < 2))
+            a.lse[row] = L == 0.f ? -INFINITY : (m[t][b] + log2f(L)) * 0.6931471805599453f;
+        }
+      }
+      ++item;
+      s = next_s;
+      g = next_g;
+      nt = next_nt;
+      continue;
     }
     // Each warp leaves its sums in a slot and goes on; kJoiners of them, in
     // turn, wait for the others' and add up.
@@ -1069,7 +1135,7 @@ cudaError_t launch_d(DecodeArgs a, int dev, int ctas, cudaStream_t st) {
          items <= clusters_at_once<D, HEADS>(dev, log_c + 1))
     ++log_c;
   if (tiles <= (int64_t)(2 * S::kWarps) << log_c &&
-      items <= clusters_at_once<D, HEADS>(dev, log_c)) {
+      items <= (log_c ? 1 : 2) * clusters_at_once<D, HEADS>(dev, log_c)) {
     a.cluster = 1 << log_c;
     return launch_pdl_smem(done_cluster, dev, q4_decode_kernel<D, HEADS, true>,
                            dim3((unsigned)items << log_c), threads, a.cluster, sizeof(S), st, a);
