@@ -4,15 +4,16 @@
 // scale.  HBM bounds it: 1.125 d bytes per (token, KV head), read once for
 // all G query heads of the group.
 //
-// Split: the work is the list of all 32-token tiles of all (sequence, KV
-// head) items, and every CTA takes an equal run of it, whatever the lengths
-// (they are known on the device only).  A run covers whole items, whose
+// Split: the work is the list of all tiles (64 tokens, 32 for short caches and
+// for 16 heads) of all (sequence, KV head) items, and every CTA takes an equal
+// run of it, whatever the lengths (they are known on the device only).  A run covers whole items, whose
 // output it writes, and at most two parts of items, whose (weighted sum,
 // maximum, sum) go to the workspace; a second kernel joins the parts of an
 // item in order.  So the workspace depends on the grid alone and the result
-// on nothing but the inputs.  Items that are short by what the table can hold,
-// and few, skip all that: each has a cluster of 1 to 8 CTAs, which join their
-// sums through shared memory.
+// on nothing but the inputs.  Two rules save item ends where items are short:
+// where they are many, a warp takes an item by itself and writes its output;
+// where they are few (and short by what the table can hold), each has a cluster
+// of 1 to 8 CTAs, which join their sums through shared memory in one launch.
 //
 // A warp takes every 12th (or 8th) tile of its CTA's run: it streams the tile's
 // codes and scales into its own ring of shared memory (cp.async, one tile
@@ -24,12 +25,12 @@
 // each lane's codes contiguous and in fragment order.
 //
 // What it measured (B200; a call's two kernels in a graph, us): 32 sequences of
-// 16384 tokens, 32 / 8 heads of 128 (604 MB) 112, 5.4 TB/s or 82 % of a plain
+// 16384 tokens, 32 / 8 heads of 128 (604 MB) 107, 5.6 TB/s or 86 % of a plain
 // copy's rate; 8 of them 37; one of 131072 37; one of 2064 6.9; 8 ragged ones
-// of 4096 to 16384, 28 / 4 heads, 19; 64 of about 2050 45.  Large calls spend
-// about as long on instructions as HBM on the bytes: without its loads the
-// kernel takes 92 of 112 us, and instructions, not latency, fill that (8, 12
-// and 16 warps are within 5 %).  Small ones are bound by the chain length ->
+// of 4096 to 16384, 28 / 4 heads, 18; 64 of about 2050 43.  Large calls spend
+// about as long on instructions as HBM on the bytes: an earlier state took 92 of
+// 112 us without its loads, and instructions, not latency, filled that (8, 12
+// and 16 warps were within 5 %).  Small ones are bound by the chain length ->
 // block -> tile -> sums -> join, about 1 us each.  Tried and slower: three or
 // four tiles ahead (no change), 16 warps at 128 registers (5 %), barriers that
 // keep a CTA's warps abreast (3 %), tokens as columns of the first product (a
@@ -57,7 +58,12 @@ constexpr int kMinTiles = 8;          // tiles per CTA, where there are few (4: 
 // at 30 and 60 on 8 sequences of 1000 to 16384 tokens (31.4, 33.0 us) and of 4096
 // (15.5 both), and at 10 (in tiles of 64) on the latter (17.6).
 constexpr int kEndTiles = 30;
-constexpr int kSoloTiles = 8;         // tiles per item on average, up to which a warp takes it alone
+// Tiles per item on average, up to which one warp takes an item by itself,
+// where there are more than two items per CTA: an item's end costs a CTA about
+// 3 us, a warp alone less than 1.  Measured with and without: 200 sequences of 0 to 700
+// tokens, 8 KV heads, 40 us and 88; 1000 of 10 to 60, 34 and 139; 64 of 1050, 27
+// and 31; 256 of 1050, 69 and 92; 64 of 2050 (33 tiles), 44.1 and 43.4.
+constexpr int kSoloTiles = 24;
 constexpr int kMaxCluster = 8;        // CTAs of an item's cluster
 constexpr float kSlack = 8.f;         // the maximum may lag by 2^8 before sums are rescaled
 constexpr int kScaleRoom = 6;         // V's scales may exceed their unit by 2^6
@@ -175,7 +181,7 @@ struct Smem {
   static constexpr int kParts = HEADS <= 8 && !CLUSTER ? 4 : 2;
   static constexpr int kWarps = D == 128 && (HEADS == 16 || !CLUSTER) ? 8 : 12;
   static constexpr int kTok = kParts * kSub;
-  static constexpr int kCodes = kSub * D / 2;           // bytes of a half tile's K (or V) codes
+  static constexpr int kCodes = kSub * D / 2;           // bytes of a part's K (or V) codes
   static constexpr int kScales = kSub * D / 16;
   static constexpr int kHalf = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
   static constexpr int kTileBytes = kParts * kHalf;
@@ -188,7 +194,7 @@ struct Smem {
   int32_t page_ok[kWarps][kStages][kParts];
   float all_o[HEADS][D], all_m[HEADS], all_l[HEADS];    // the CTA's sums, for its cluster
   int64_t scan[kWarps];
-  int64_t where[2];                                     // sequence of the run's start, units before it
+  int64_t where[2];                                     // the run's start: sequence, place in it
 };
 
 // The partial of a part: [G][D] weighted sums, then G maxima and G sums;
@@ -255,7 +261,7 @@ __device__ inline int cta_of(int64_t unit, int64_t total, int ctas) {
 
 // Of a warp's lanes, r = lane / 4 and c = lane % 4.  The first product has
 // tokens as rows and heads as columns, so a lane holds the logits of two
-// tokens of each half tile for heads 2 c and 2 c + 1; a transpose of the
+// tokens of each part of a tile for heads 2 c and 2 c + 1; a transpose of the
 // scaled weights (movmatrix) makes them the second product's operand, whose
 // rows are dimensions and whose columns are the heads again.  Up to 4 heads
 // use the columns twice: 0 - 3 weigh with V's scale of the even group, 4 - 7
@@ -462,8 +468,9 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
     }
   };
 
-  // ---- prefetching: this warp's tiles u0 + warp, + kWarps, ..  A half warp
-  // copies a half tile, whose page it looks up one tile ahead.
+  // ---- prefetching: this warp's tiles u0 + warp, + kWarps, .. (solo: all of its
+  // items).  A half warp copies every other part of a tile, whose pages it looks
+  // up one tile ahead.
   int p_left = 0;                          // tiles not yet issued
   if (solo)
     p_left = my_items > 0 ? 0x7fffffff : 0;            // until the items have run out
@@ -1127,7 +1134,8 @@ cudaError_t launch_d(DecodeArgs a, int dev, int ctas, cudaStream_t st) {
   // 2064 tokens, 8 KV heads: 6.9 us against 9.0; 16 x 300 to 600: 7.6 against 12.9).
   // By what the table can hold, the lengths being on the device: as many CTAs as
   // give every warp one tile, while all clusters run at once (16 clusters of 8,
-  // one too many: 13.0 us against 9.3), and at most two tiles per warp.
+  // one too many: 13.0 us against 9.3), and at most two tiles per warp.  Items of
+  // one CTA may take two rounds (30 x 100 to 700: 13.8 us against 20.5).
   const int64_t items = (int64_t)a.nseq * a.c.Hkv;
   const int64_t tiles = (((int64_t)a.width << a.c.log_bs) + S::kTok - 1) / S::kTok;
   int log_c = 0;

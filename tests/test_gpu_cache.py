@@ -949,3 +949,33 @@ def test_attend_short_and_wide_tables(nseq, Hq, Hkv, d, hi):
         a = _check_attend(q, pool, t, lens, kv)
         b = api.q4_decode_attention(q, pool, t, _i32(lens), True)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("nseq,Hq,Hkv,d,hi", [
+    (45, 32, 8, 128, 900), (310, 4, 1, 64, 90), (32, 48, 12, 64, 300), (100, 28, 4, 128, 500),
+    (80, 64, 4, 128, 200), (330, 16, 1, 64, 260)])
+def test_attend_many_short_items(nseq, Hq, Hkv, d, hi):
+    """More than two short items per CTA, on tables too wide for clusters: a
+    warp takes each by itself.  Empty sequences and pages that are missing
+    among them."""
+    rng = np.random.default_rng(nseq + hi)
+    lens = rng.integers(0, hi + 1, nseq).tolist()
+    lens[0], lens[3], lens[nseq - 1] = 0, hi, 1
+    g = _gen(nseq + hi)
+    pool, table, kv = _fill(g, lens, Hkv, d, 16)
+    wide = torch.full((nseq, 9000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = _bf(g, nseq, Hq, d)
+    a = _check_attend(q, pool, wide, lens, kv)
+    b = api.q4_decode_attention(q, pool, wide, _i32(lens), True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    wide[3, 0] = pool.shape[0]                     # the first page of a long one is missing
+    status = _i32([0])
+    out, lse = api.q4_decode_attention(q, pool, wide, _i32(lens), True, status=status)
+    assert int(status) == _lib.DEV_BAD_INDEX
+    ref, rl = co.q4_decode_attention(_f64(q[3]), *(x[:, 16:] for x in kv[3]))
+    mag, _ = co.q4_decode_attention(_f64(q[3]), kv[3][0][:, 16:], np.abs(kv[3][1][:, 16:]))
+    assert np.all(np.abs(_f64(out[3]) - ref) <= BF * np.abs(ref) + 2.0 ** -10 * mag)
+    assert np.all(np.abs(_f64(lse[3]) - rl) <= 2.0 ** -13)
+    keep = [i for i in range(nseq) if i != 3]
+    assert torch.equal(out[keep], a[0][keep]) and torch.equal(lse[keep], a[1][keep])
