@@ -25,7 +25,7 @@
 // each lane's codes contiguous and in fragment order.
 //
 // What it measured (B200; a call's two kernels in a graph, us): 32 sequences of
-// 16384 tokens, 32 / 8 heads of 128 (604 MB) 107 to 113 by the box's clock, 5.3
+// 16384 tokens, 32 / 8 heads of 128 (604 MB) 107 to 113 from one GPU to another, 5.3
 // TB/s or more and 82 % of a plain copy's rate; 8 of them 37; one of 131072 37; one of 2064 6.9; 8 ragged ones
 // of 4096 to 16384, 28 / 4 heads, 18; 64 of about 2050 43.  Large calls spend
 // about as long on instructions as HBM on the bytes: an earlier state took 92 of
