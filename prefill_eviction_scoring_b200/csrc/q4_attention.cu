@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
 #pragma unroll
     for (int h = 0; h < kParts / 2; ++h) { // a tile's later parts may lie past the end
       const int j = p_tile * kTok + (half + 2 * h) * kSub;
-      p_block[h] = j < p_n ? __ldg(p_row + (j >> log_bs)) : -2;
+      p_block[h] = j < p_n ? __ldg(p_row + (j >> log_bs)) : -1;
     }
   };
   if (p_left > 0) {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(32 * Smem<D, HEADS, CLUSTER>::kWarps, 1)
             cp_async16(dst + (D == 128 && i >= 2 ? v_dst ^ 32 : v_dst) + i * 64, vc + i * 256);
           }
           if (D == 128 || hl < D / 8) cp_async16(dst + sc_dst, page + sc_src + off * (D / 16));
-        } else if (a.status && p_block[h] != -2 && hl == 0) {
+        } else if (a.status && hl == 0 && p_tile * kTok + (half + 2 * h) * kSub < p_n) {
           atomicOr(a.status, WAITS_DEV_BAD_INDEX);
         }
       }

@@ -482,6 +482,26 @@ def test_attend_bad_table_entries_are_left_out():
     assert not out.any() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("entry", [-1, -2, -2 ** 31])
+@pytest.mark.parametrize("columns", [2, 9000])
+@pytest.mark.parametrize("n", [17, 32])
+def test_attend_every_negative_table_entry_sets_the_status(entry, columns, n):
+    g = _gen(23)
+    pool, table, _ = _fill(g, [n], 1, 64, 16)
+    wide = torch.full((1, columns), entry, dtype=torch.int32, device="cuda")
+    wide[:, :2] = table[:, :2]
+    status = _i32([0])
+    q = _bf(g, 1, 2, 64)
+    a = api.q4_decode_attention(q, pool, wide, _i32([n]), status=status)
+    assert int(status) == 0                        # entries past the length are not looked at
+    wide[0, 1] = entry
+    b = api.q4_decode_attention(q, pool, wide, _i32([n]), status=status)
+    assert int(status) == _lib.DEV_BAD_INDEX
+    assert not torch.equal(a, b)
+    c = api.q4_decode_attention(q, pool, wide, _i32([16]))
+    assert torch.equal(b, c)
+
+
 def test_attend_lengths_out_of_range_are_clamped():
     g = _gen(22)
     pool, table, kv = _fill(g, [64, 64], 2, 64, 16)
