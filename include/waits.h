@@ -438,7 +438,7 @@ waits_status waits_qk_norm_rope(int32_t num_tokens, int32_t num_q_heads, int32_t
  *          written with scale = bf16(max|x| / 6) and code = x / scale to the
  *          nearest, ties to the even code, at most 6.  A group whose scale
  *          would be below 2^-126 is written as zeros, one that holds an
- *          infinity or a NaN gets a NaN scale.
+ *          infinity or a NaN gets a NaN scale.  Scales are never negative.
  *   codes  low nibble first, the pair of dimensions (i, i + 1), i even, at
  *          byte (K) c * d/8 + 2 s + h, i = 16 s + 4 c + 2 h, c, h < (4, 2);
  *               (V) r * d/16 + 2 g + h, i = 32 g + 4 r + 2 h, r, h < (8, 2)
